@@ -70,7 +70,9 @@ typedef enum {
   MOE_ERR_DEVICE = 4       /* no usable gfx950 device or a launch failed   */
 } moe_status;
 
-typedef enum { MOE_SRC_BF16 = 0, MOE_SRC_FP32 = 1 } moe_src_dtype;
+/* Element types of plain matrices.  fp16 is taken by the MXFP4 conversions,
+ * moe_linear_mx4 and the row operators below, not by moe_quantize_act. */
+typedef enum { MOE_SRC_BF16 = 0, MOE_SRC_FP32 = 1, MOE_SRC_FP16 = 2 } moe_src_dtype;
 
 /* Layer shape.  d_model and d_ff: multiples of 128.  1 <= num_experts <= 1024.
  * 1 <= top_k <= min(32, num_experts).  0 <= num_shared <= 8.
@@ -261,6 +263,118 @@ moe_status moe_latent_tail(int64_t num_tokens, int32_t latent, int32_t hidden, f
  * num_tokens == 0 enqueues nothing.  Errors and streams as for moe_forward. */
 moe_status moe_router_bias_update(const moe_plan_t *plan, const int32_t *expert_offsets,
                                   int64_t num_tokens, float rate, float *router_b, void *stream);
+
+/* ---- The layer's pieces on their own -----------------------------------
+ * For layers that moe_forward does not cover: another activation between the
+ * projections, another router, training.  A forward is then
+ *   moe_sort_tokens -> (moe_quantize_mx4) -> moe_dispatch_rows of the tokens'
+ *   rows, or of their codes and scales -> moe_linear_mx4 with the order's
+ *   offsets -> the caller's activation -> moe_quantize_mx4 -> moe_linear_mx4
+ *   -> moe_combine_rows.
+ * Errors and streams as for moe_forward.  What device memory holds (ids, row
+ * numbers, offsets) cannot be checked on the host: values outside their range
+ * are treated as said at each call and never reach outside a buffer. */
+
+/* MXFP4-quantise rows of a bf16, fp16 or fp32 matrix along its columns: per
+ * row and per 32 consecutive columns, e = clamp(floor(log2 amax) - 2, -127,
+ * 127) (amax == 0 -> -127), codes = E2M1 round-to-nearest-even of v / 2^e with
+ * saturation to +-6 (sign kept on zero), scale byte = e + 127.  A block with
+ * an infinity or a NaN gets the scale 255 (NaN) and zero codes.
+ * src [rows][ld_src] (elements); codes [rows][cols/2] (element 2i in the low
+ * nibble of byte i), scales [rows][cols/32]: the canonical form of the expert
+ * weights.  cols % 32 == 0 (else MOE_ERR_UNSUPPORTED), ld_src >= cols,
+ * rows <= 2^40, cols <= 2^30; src aligned to its element, codes to 4 bytes.
+ * Rows on 16 bytes are the fast case. */
+moe_status moe_quantize_mx4(const void *src, moe_src_dtype dt, int64_t rows, int64_t cols,
+                            int64_t ld_src, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values of an MXFP4 matrix in canonical form, code * 2^(scale - 127)
+ * rounded to nearest even to dt (exact in bf16 and fp32 except that 4 and 6
+ * times 2^127 are infinite); a block with scale 255 is NaN.  Arguments as for
+ * moe_quantize_mx4, dst [rows][ld_dst]. */
+moe_status moe_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                              int64_t cols, void *dst, moe_src_dtype dt, int64_t ld_dst,
+                              void *stream);
+
+/* Product of MXFP4 matrices: y[r][j] = sum over i < k of A[r][i] W_e[j][i],
+ * fp32 accumulation, rounded once to dt.  A: a_codes [rows][k/2], a_scales
+ * [rows][k/32]; W: w_codes [mats][n][k/2], w_scales [mats][n][k/32], all in
+ * canonical form; y [rows][ld_y], ld_y >= n.
+ * offsets == NULL: mats must be 1 and W_0 is taken for every row.  Otherwise
+ * int32 [mats+1] on the device, not decreasing: W_e is taken for the rows
+ * offsets[e] <= r < offsets[e+1] (moe_sort_tokens' offsets, moe_forward's
+ * expert_offsets tap); rows before the first and from the last offset on are
+ * neither read nor written.  Offsets outside [0, rows] are taken as the
+ * nearer end; a matrix whose end lies before its start has no rows; ranges
+ * that overlap give undefined values in the rows that they share.
+ * A block with scale 255 makes the sums it enters NaN.
+ * 0 <= rows <= 2^25 and 0 <= n (0: nothing is enqueued); 1 <= mats <= 1024;
+ * k a multiple of 32 in 32 .. 65536, n <= 2^20, else MOE_ERR_UNSUPPORTED.
+ * a_codes and w_codes 16-byte, offsets 4-byte aligned, y aligned to its
+ * element.  k a multiple of 512 (then 128) is the fast case. */
+moe_status moe_linear_mx4(const uint8_t *a_codes, const uint8_t *a_scales, int64_t rows,
+                          const uint8_t *w_codes, const uint8_t *w_scales, int32_t mats,
+                          const int32_t *offsets, int64_t n, int64_t k, void *y, moe_src_dtype dt,
+                          int64_t ld_y, void *stream);
+
+typedef enum { MOE_ID_INT32 = 0, MOE_ID_INT64 = 1 } moe_id_dtype;
+
+/* The order of tokens sorted by expert.  Pair p = t*top_k + j is token t's
+ * j-th choice ids[p]; a choice outside [0, num_experts) (-1 for padding) is
+ * dropped.  The kept pairs are sorted by expert, pairs of an expert in
+ * ascending order (a token that names an expert twice has two rows):
+ *   offsets   [num_experts+1] first row of each expert; the last is the
+ *             number of rows
+ *   row_src   [num_tokens*top_k] pair of each row; -1 from the number of rows on
+ *   token_row [num_tokens][top_k] row of each pair; -1 for a dropped pair
+ * 0 <= num_tokens <= 2^20 (0: only offsets are written, all zero);
+ * 1 <= top_k <= 32; 1 <= num_experts <= 1024.  Buffers aligned to their
+ * elements.  workspace: moe_sort_tokens_workspace_bytes bytes (0 for few
+ * pairs: then it may be NULL), 256-byte aligned, contents on entry
+ * irrelevant; concurrent calls need distinct workspaces. */
+moe_status moe_sort_tokens_workspace_bytes(int64_t num_tokens, int32_t top_k, int32_t num_experts,
+                                           size_t *out_bytes);
+moe_status moe_sort_tokens(const void *ids, moe_id_dtype id_dt, int64_t num_tokens, int32_t top_k,
+                           int32_t num_experts, int32_t *offsets, int32_t *row_src,
+                           int32_t *token_row, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Rows sorted by expert from the tokens' rows: xs[token_row[t][j]] = x[t], a
+ * copy of row_bytes bytes (any element type; MXFP4 codes and scales are two
+ * calls).  ld_x and ld_xs in bytes, >= row_bytes.  xs has rows_cap rows; an
+ * entry of token_row outside [0, rows_cap) is skipped, and two equal ones
+ * leave either copy.  num_rows (one int32 on the device, moe_sort_tokens'
+ * offsets + num_experts) or NULL: rows from *num_rows on are zero-filled, with
+ * NULL rows that no pair has are left as they were.  num_tokens == 0 or
+ * row_bytes == 0 enqueues nothing.  x and xs must not overlap. */
+moe_status moe_dispatch_rows(const void *x, int64_t row_bytes, int64_t ld_x,
+                             const int32_t *token_row, int64_t num_tokens, int32_t top_k,
+                             const int32_t *num_rows, int64_t rows_cap, void *xs, int64_t ld_xs,
+                             void *stream);
+
+/* Back to the tokens: y[t] = sum over j of w[t][j] rows[token_row[t][j]], in
+ * fp32 in ascending j, rounded once to dt; w fp32 [num_tokens][top_k], or NULL
+ * for ones (which is moe_dispatch_rows' gradient: x's from xs').  Entries of
+ * token_row outside [0, rows_cap) add nothing (no row is read for them); a
+ * token without rows gets zeros.  rows [rows_cap][ld_rows] and y
+ * [num_tokens][ld_y] of type dt, d columns.  num_tokens == 0 or d == 0
+ * enqueues nothing. */
+moe_status moe_combine_rows(const void *rows, moe_src_dtype dt, int64_t rows_cap, int64_t d,
+                            int64_t ld_rows, const int32_t *token_row, const float *w,
+                            int64_t num_tokens, int32_t top_k, void *y, int64_t ld_y, void *stream);
+
+/* Gradients of moe_combine_rows from dy [num_tokens][ld_dy]:
+ *   drows[token_row[t][j]] = w[t][j] dy[t], rounded once to dt (NULL: skipped)
+ *   dw[t][j] = sum over columns of dy[t] rows[token_row[t][j]], fp32, and 0
+ *              for an entry outside [0, rows_cap) (NULL: skipped, and rows
+ *              may be NULL)
+ * num_rows as in moe_dispatch_rows, for drows.  With w NULL drows is a copy of
+ * dy's rows.  Fixed orders of summation: equal calls give equal bytes. */
+moe_status moe_combine_rows_backward(const void *dy, const void *rows, moe_src_dtype dt,
+                                     int64_t rows_cap, int64_t d, int64_t ld_dy, int64_t ld_rows,
+                                     const int32_t *token_row, const float *w, int64_t num_tokens,
+                                     int32_t top_k, const int32_t *num_rows, void *drows,
+                                     int64_t ld_drows, float *dw, void *stream);
 
 /* Stages of moe_forward, for per-stage timing. */
 typedef enum {

@@ -30,7 +30,7 @@ FLAGS = [
 
 LIBS = {
     "libmxmoe.so": ["api.cpp", "kernels_route.hip", "kernels_gemm.hip", "kernels_pack.hip",
-                    "kernels_tail.hip"],
+                    "kernels_tail.hip", "kernels_mx4.hip", "kernels_linear.hip", "kernels_tokens.hip"],
     "libmxmoe_inputs.so": ["gen_inputs.hip"],
 }
 

@@ -634,3 +634,212 @@ moe_status moe_profile_end(moe_plan_t* plan, double* stage_ms, int32_t* calls) {
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The layer's pieces on their own
+// ---------------------------------------------------------------------------
+namespace {
+
+// the kernels' element type and its size; false for a value of no type
+bool row_type(moe_src_dtype dt, RowType& t, int64_t& sz) {
+  switch (dt) {
+    case MOE_SRC_BF16: t = RowType::kBf16; sz = 2; return true;
+    case MOE_SRC_FP32: t = RowType::kFp32; sz = 4; return true;
+    case MOE_SRC_FP16: t = RowType::kFp16; sz = 2; return true;
+  }
+  return false;
+}
+
+moe_status launched(hipError_t e) {
+  if (e != hipSuccess) return fail(MOE_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return MOE_OK;
+}
+
+// shared checks of the two MXFP4 conversions
+moe_status check_mx4(const void* plain, moe_src_dtype dt, int64_t rows, int64_t cols, int64_t ld, const uint8_t* codes,
+                     const uint8_t* scales, RowType& t) {
+  int64_t sz;
+  if (!row_type(dt, t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "negative size");
+  if (cols % 32) return fail(MOE_ERR_UNSUPPORTED, "cols (%lld) must be a multiple of 32", static_cast<long long>(cols));
+  if (rows > (int64_t(1) << 40) || cols > (int64_t(1) << 30) || ld > (int64_t(1) << 40))
+    return fail(MOE_ERR_UNSUPPORTED, "rows above 2^40, cols above 2^30 or row stride above 2^40");
+  if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "row stride < cols");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!plain || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(plain, sz) || !aligned(codes, 4))
+    return fail(MOE_ERR_INVALID_ARG, "the plain matrix needs the alignment of its elements, codes 4 bytes");
+  return MOE_OK;
+}
+
+moe_status check_order(int64_t T, int32_t k) {
+  if (T < 0 || T > (int64_t(1) << 20)) return fail(MOE_ERR_INVALID_ARG, "num_tokens outside [0, 2^20]");
+  if (k < 1 || k > 32) return fail(MOE_ERR_INVALID_ARG, "top_k outside [1, 32]");
+  return MOE_OK;
+}
+
+moe_status check_sort(int64_t T, int32_t k, int32_t E) {
+  moe_status s = check_order(T, k);
+  if (s != MOE_OK) return s;
+  if (E < 1 || E > 1024) return fail(MOE_ERR_INVALID_ARG, "num_experts outside [1, 1024]");
+  return MOE_OK;
+}
+
+size_t sort_workspace(int64_t pairs, int32_t E) {
+  if (pairs <= kSortSmallPairs) return 0;
+  const int64_t chunk = sort_chunk(pairs);
+  return size_t((pairs + chunk - 1) / chunk) * E * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_mx4(const void* src, moe_src_dtype dt, int64_t rows, int64_t cols, int64_t ld_src,
+                            uint8_t* codes, uint8_t* scales, void* stream) {
+  RowType t;
+  moe_status s = check_mx4(src, dt, rows, cols, ld_src, codes, scales, t);
+  if (s != MOE_OK || rows == 0 || cols == 0) return s;
+  s = check_device();
+  if (s != MOE_OK) return s;
+  return launched(launch_quantize_mx4(src, t, rows, cols, ld_src, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* dst,
+                              moe_src_dtype dt, int64_t ld_dst, void* stream) {
+  RowType t;
+  moe_status s = check_mx4(dst, dt, rows, cols, ld_dst, codes, scales, t);
+  if (s != MOE_OK || rows == 0 || cols == 0) return s;
+  s = check_device();
+  if (s != MOE_OK) return s;
+  return launched(launch_dequantize_mx4(codes, scales, rows, cols, dst, t, ld_dst, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_linear_mx4(const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows, const uint8_t* w_codes,
+                          const uint8_t* w_scales, int32_t mats, const int32_t* offsets, int64_t n, int64_t k, void* y,
+                          moe_src_dtype dt, int64_t ld_y, void* stream) {
+  RowType t;
+  int64_t sz;
+  if (!row_type(dt, t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  if (rows < 0 || n < 0 || k <= 0 || mats <= 0) return fail(MOE_ERR_INVALID_ARG, "negative size, or k or mats not positive");
+  if (!offsets && mats != 1) return fail(MOE_ERR_INVALID_ARG, "%d matrices need offsets", mats);
+  if (k % 32 || k > 65536) return fail(MOE_ERR_UNSUPPORTED, "k (%lld) must be a multiple of 32, at most 65536", static_cast<long long>(k));
+  if (mats > 1024 || n > (1 << 20) || rows > (1 << 25))
+    return fail(MOE_ERR_UNSUPPORTED, "more than 1024 matrices, 2^20 columns or 2^25 rows");
+  if (ld_y < n) return fail(MOE_ERR_INVALID_ARG, "ld_y < n");
+  if (ld_y > (int64_t(1) << 32)) return fail(MOE_ERR_UNSUPPORTED, "ld_y above 2^32");
+  if (rows == 0 || n == 0) return MOE_OK;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !y) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(y, sz) || (offsets && !aligned(offsets, 4)))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer (codes: 16 bytes; offsets: 4; y: its element)");
+  int num_cus = 0;
+  moe_status s = check_device(&num_cus);
+  if (s != MOE_OK) return s;
+  const LinearArgs a{a_codes, a_scales, w_codes, w_scales, offsets, rows, mats, static_cast<int>(n),
+                     static_cast<int>(k), y, ld_y, num_cus > 0 ? num_cus : 256};
+  return launched(launch_linear_mx4(a, t, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_sort_tokens_workspace_bytes(int64_t num_tokens, int32_t top_k, int32_t num_experts, size_t* out_bytes) {
+  if (!out_bytes) return fail(MOE_ERR_INVALID_ARG, "out_bytes is NULL");
+  moe_status s = check_sort(num_tokens, top_k, num_experts);
+  if (s != MOE_OK) return s;
+  *out_bytes = sort_workspace(num_tokens * top_k, num_experts);
+  return MOE_OK;
+}
+
+moe_status moe_sort_tokens(const void* ids, moe_id_dtype id_dt, int64_t num_tokens, int32_t top_k, int32_t num_experts,
+                           int32_t* offsets, int32_t* row_src, int32_t* token_row, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (id_dt != MOE_ID_INT32 && id_dt != MOE_ID_INT64) return fail(MOE_ERR_INVALID_ARG, "bad id dtype");
+  moe_status s = check_sort(num_tokens, top_k, num_experts);
+  if (s != MOE_OK) return s;
+  if (!offsets || (num_tokens > 0 && (!ids || !row_src || !token_row))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(ids, id_dt == MOE_ID_INT64 ? 8 : 4) || !aligned(offsets, 4) || !aligned(row_src, 4) || !aligned(token_row, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer");
+  const int64_t pairs = num_tokens * top_k;
+  const size_t need = sort_workspace(pairs, num_experts);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s", need, workspace_bytes, workspace ? "" : " (NULL)");
+  if (need && !aligned(workspace, 256)) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  s = check_device();
+  if (s != MOE_OK) return s;
+  return launched(launch_sort_tokens(ids, id_dt == MOE_ID_INT64, pairs, num_experts, offsets, row_src, token_row,
+                                     static_cast<int*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_dispatch_rows(const void* x, int64_t row_bytes, int64_t ld_x, const int32_t* token_row,
+                             int64_t num_tokens, int32_t top_k, const int32_t* num_rows, int64_t rows_cap, void* xs,
+                             int64_t ld_xs, void* stream) {
+  moe_status s = check_order(num_tokens, top_k);
+  if (s != MOE_OK) return s;
+  if (row_bytes < 0 || rows_cap < 0) return fail(MOE_ERR_INVALID_ARG, "negative size");
+  if (ld_x < row_bytes || ld_xs < row_bytes) return fail(MOE_ERR_INVALID_ARG, "row stride < row_bytes");
+  if (ld_x > (int64_t(1) << 32) || ld_xs > (int64_t(1) << 32) || rows_cap > (1 << 25))
+    return fail(MOE_ERR_UNSUPPORTED, "row stride above 2^32 bytes or more than 2^25 rows");
+  if (num_tokens == 0 || row_bytes == 0) return MOE_OK;
+  if (!x || !token_row || (rows_cap > 0 && !xs)) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(token_row, 4) || !aligned(num_rows, 4)) return fail(MOE_ERR_INVALID_ARG, "misaligned token_row or num_rows");
+  s = check_device();
+  if (s != MOE_OK) return s;
+  return launched(launch_dispatch_rows(x, row_bytes, ld_x, token_row, num_tokens, top_k, rows_cap, num_rows, xs, ld_xs,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_combine_rows(const void* rows, moe_src_dtype dt, int64_t rows_cap, int64_t d, int64_t ld_rows,
+                            const int32_t* token_row, const float* w, int64_t num_tokens, int32_t top_k, void* y,
+                            int64_t ld_y, void* stream) {
+  RowType t;
+  int64_t sz;
+  if (!row_type(dt, t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  moe_status s = check_order(num_tokens, top_k);
+  if (s != MOE_OK) return s;
+  if (rows_cap < 0 || d < 0) return fail(MOE_ERR_INVALID_ARG, "negative size");
+  if (ld_rows < d || ld_y < d) return fail(MOE_ERR_INVALID_ARG, "row stride < d");
+  if (ld_rows > (int64_t(1) << 32) || ld_y > (int64_t(1) << 32) || rows_cap > (1 << 25))
+    return fail(MOE_ERR_UNSUPPORTED, "row stride above 2^32 or more than 2^25 rows");
+  if (num_tokens == 0 || d == 0) return MOE_OK;
+  if (!token_row || !y || (rows_cap > 0 && !rows)) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(rows, sz) || !aligned(y, sz) || !aligned(token_row, 4) || !aligned(w, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer");
+  s = check_device();
+  if (s != MOE_OK) return s;
+  CombineArgs a{};
+  a.T = num_tokens; a.R = rows_cap; a.d = d; a.k = top_k;
+  a.rows = rows; a.ld = ld_rows;
+  a.token_row = token_row; a.w = w;
+  a.y = y; a.ld_y = ld_y;
+  return launched(launch_combine_rows(a, t, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_combine_rows_backward(const void* dy, const void* rows, moe_src_dtype dt, int64_t rows_cap, int64_t d,
+                                     int64_t ld_dy, int64_t ld_rows, const int32_t* token_row, const float* w,
+                                     int64_t num_tokens, int32_t top_k, const int32_t* num_rows, void* drows,
+                                     int64_t ld_drows, float* dw, void* stream) {
+  RowType t;
+  int64_t sz;
+  if (!row_type(dt, t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  moe_status s = check_order(num_tokens, top_k);
+  if (s != MOE_OK) return s;
+  if (rows_cap < 0 || d < 0) return fail(MOE_ERR_INVALID_ARG, "negative size");
+  if (ld_dy < d || (dw && ld_rows < d) || (drows && ld_drows < d)) return fail(MOE_ERR_INVALID_ARG, "row stride < d");
+  if (ld_dy > (int64_t(1) << 32) || ld_rows > (int64_t(1) << 32) || ld_drows > (int64_t(1) << 32) || rows_cap > (1 << 25))
+    return fail(MOE_ERR_UNSUPPORTED, "row stride above 2^32 or more than 2^25 rows");
+  if (num_tokens == 0 || (!drows && !dw)) return MOE_OK;
+  if (!token_row || (d > 0 && !dy) || (d > 0 && dw && rows_cap > 0 && !rows)) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(dy, sz) || !aligned(rows, sz) || !aligned(drows, sz) || !aligned(token_row, 4) || !aligned(w, 4) ||
+      !aligned(dw, 4) || !aligned(num_rows, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer");
+  s = check_device();
+  if (s != MOE_OK) return s;
+  CombineArgs a{};
+  a.T = num_tokens; a.R = rows_cap; a.d = d; a.k = top_k;
+  a.rows = dw ? rows : nullptr; a.ld = ld_rows;
+  a.token_row = token_row; a.w = w;
+  a.dy = dy; a.ld_y = ld_dy;
+  a.drows = drows; a.ld_d = ld_drows;
+  a.dw = dw; a.num_rows = num_rows;
+  return launched(launch_combine_rows_backward(a, t, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

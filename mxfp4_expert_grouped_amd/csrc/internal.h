@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace mxmoe {
 
 // One unit of grouped-GEMM work: rows [row_begin, row_end) of expert `ex`
@@ -165,6 +167,60 @@ hipError_t launch_gemm_down(const FwdArgs& a, hipStream_t st);
 hipError_t launch_combine(const FwdArgs& a, hipStream_t st);
 hipError_t launch_pack_mx4(const uint8_t* codes, const uint8_t* scales, int64_t mats, int64_t rows,
                            int64_t k, int interleave, uint8_t* codes_p, uint8_t* scales_p, hipStream_t st);
+
+// ---- the standalone pieces: MXFP4 conversion and product, token order
+
+// element types of rows (row_types.h)
+enum class RowType { kBf16, kFp16, kFp32 };
+
+hipError_t launch_quantize_mx4(const void* src, RowType dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                               uint8_t* scales, hipStream_t st);
+hipError_t launch_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* dst,
+                                 RowType dt, int64_t ld, hipStream_t st);
+
+// y[r] = A[r] W[e(r)]^T, both MXFP4 in canonical layout (all device pointers)
+struct LinearArgs {
+  const uint8_t *a_c, *a_s;  // [rows][k/2], [rows][k/32]
+  const uint8_t *w_c, *w_s;  // [mats][n][k/2], [mats][n][k/32]
+  const int* offsets;        // [mats+1] first row of each matrix, or null: all rows to one matrix
+  int64_t rows;
+  int mats, n, k;
+  void* y;                   // [rows][ld_y]
+  int64_t ld_y;
+  int num_cus;
+};
+hipError_t launch_linear_mx4(const LinearArgs& a, RowType dt, hipStream_t st);
+
+// pairs sorted by one workgroup in one launch
+constexpr int kSortSmallPairs = 4096;
+// pairs per workgroup above that: at least 2048, and at most 512 chunks, so
+// that summing the counts along the chunks stays short
+inline int sort_chunk(int64_t pairs) {
+  const int64_t c = (pairs + 511) / 512;
+  return static_cast<int>(std::max<int64_t>(2048, (c + 1023) / 1024 * 1024));
+}
+hipError_t launch_sort_tokens(const void* ids, bool ids64, int64_t pairs, int E, int* offsets, int* row_src,
+                              int* token_row, int* counts, hipStream_t st);
+hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t ld_x, const int* token_row, int64_t T, int k,
+                                int64_t R, const int* num_rows, void* out, int64_t ld_out, hipStream_t st);
+
+struct CombineArgs {
+  int64_t T, R, d;           // tokens, rows that there are, columns
+  int k;
+  const void* rows;          // [R][ld]
+  int64_t ld;
+  const int* token_row;      // [T][k]
+  const float* w;            // [T][k], or null: ones
+  void* y;                   // forward: [T][ld_y]
+  const void* dy;            // backward: [T][ld_y]
+  int64_t ld_y;
+  void* drows;               // backward: [R][ld_d], or null
+  int64_t ld_d;
+  float* dw;                 // backward: [T][k], or null
+  const int* num_rows;       // backward: first row of drows to zero-fill, or null
+};
+hipError_t launch_combine_rows(const CombineArgs& a, RowType dt, hipStream_t st);
+hipError_t launch_combine_rows_backward(const CombineArgs& a, RowType dt, hipStream_t st);
 
 // bytes of one packed scale matrix [rows/16][ceil(k/512)][64][4]
 __host__ __device__ inline int64_t packed_scale_bytes(int64_t rows, int64_t k) { return rows * (k / 32); }

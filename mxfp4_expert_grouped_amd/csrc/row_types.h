@@ -1,0 +1,76 @@
+// The element types of rows (bf16, fp16, fp32), eight elements at a time.
+// Arithmetic is fp32 throughout; a store rounds once, to nearest even.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mxmoe {
+
+typedef __bf16 bf16_t;
+
+// The conversions are the compiler's: V_CVT_PK_BF16_F32 and V_CVT_F16_F32
+// round to nearest even and keep NaN, infinities and subnormal numbers.
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) { return static_cast<float>(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float f) { return static_cast<T>(f); }
+
+// two elements of a 16-bit type as one dword, the first in the low half
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef T v2 __attribute__((ext_vector_type(2)));
+  const v2 v = {static_cast<T>(a), static_cast<T>(b)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b);
+template <>
+__device__ __forceinline__ void unpack2<bf16_t>(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ void unpack2<_Float16>(uint32_t w, float& a, float& b) {
+  a = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w)));
+  b = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w >> 16)));
+}
+
+// eight consecutive elements; ALIGNED: p is on 16 bytes
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  if constexpr (!ALIGNED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    unpack2<T>(a.x, v[0], v[1]);
+    unpack2<T>(a.y, v[2], v[3]);
+    unpack2<T>(a.z, v[4], v[5]);
+    unpack2<T>(a.w, v[6], v[7]);
+  }
+}
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+  if constexpr (!ALIGNED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = from_f32<T>(v[i]);
+  } else if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+  }
+}
+
+// whether every row of a matrix starts on `a` bytes
+inline bool rows_aligned(const void* p, int64_t ld_bytes, int64_t a) {
+  return reinterpret_cast<uintptr_t>(p) % a == 0 && ld_bytes % a == 0;
+}
+
+}  // namespace mxmoe

@@ -15,12 +15,16 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmxmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
-MOE_SRC_BF16, MOE_SRC_FP32 = 0, 1
+MOE_SRC_BF16, MOE_SRC_FP32, MOE_SRC_FP16 = 0, 1, 2
+MOE_ID_INT32, MOE_ID_INT64 = 0, 1
 
 EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_quantize_act",
             "moe_forward", "moe_forward_noalloc", "moe_profile_begin", "moe_profile_end", "moe_packed_scale_bytes",
             "moe_pack_mx4", "moe_latent_tail_workspace_bytes", "moe_latent_tail",
             "moe_router_bias_update",
+            "moe_quantize_mx4", "moe_dequantize_mx4", "moe_linear_mx4",
+            "moe_sort_tokens_workspace_bytes", "moe_sort_tokens", "moe_dispatch_rows",
+            "moe_combine_rows", "moe_combine_rows_backward",
             "moe_status_string", "moe_last_error")
 STAGES = ("router", "topk", "permute", "gate_up", "down", "combine")
 
@@ -115,6 +119,30 @@ def load_library(path: str = LIB_PATH):
     lib.moe_latent_tail.restype = c_int
     lib.moe_router_bias_update.argtypes = [c_void_p, c_void_p, c_int64, ctypes.c_float, c_void_p, c_void_p]
     lib.moe_router_bias_update.restype = c_int
+    lib.moe_quantize_mx4.argtypes = [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                     c_void_p]
+    lib.moe_quantize_mx4.restype = c_int
+    lib.moe_dequantize_mx4.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int, c_int64,
+                                       c_void_p]
+    lib.moe_dequantize_mx4.restype = c_int
+    lib.moe_linear_mx4.argtypes = [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int32, c_void_p,
+                                   c_int64, c_int64, c_void_p, c_int, c_int64, c_void_p]
+    lib.moe_linear_mx4.restype = c_int
+    lib.moe_sort_tokens_workspace_bytes.argtypes = [c_int64, c_int32, c_int32, POINTER(c_size_t)]
+    lib.moe_sort_tokens_workspace_bytes.restype = c_int
+    lib.moe_sort_tokens.argtypes = [c_void_p, c_int, c_int64, c_int32, c_int32, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_size_t, c_void_p]
+    lib.moe_sort_tokens.restype = c_int
+    lib.moe_dispatch_rows.argtypes = [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int32, c_void_p,
+                                      c_int64, c_void_p, c_int64, c_void_p]
+    lib.moe_dispatch_rows.restype = c_int
+    lib.moe_combine_rows.argtypes = [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                     c_int64, c_int32, c_void_p, c_int64, c_void_p]
+    lib.moe_combine_rows.restype = c_int
+    lib.moe_combine_rows_backward.argtypes = [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64,
+                                              c_int64, c_void_p, c_void_p, c_int64, c_int32, c_void_p,
+                                              c_void_p, c_int64, c_void_p, c_void_p]
+    lib.moe_combine_rows_backward.restype = c_int
     lib.moe_status_string.argtypes = [c_int]
     lib.moe_status_string.restype = c_char_p
     lib.moe_last_error.argtypes = []
@@ -212,3 +240,56 @@ def moe_latent_tail(num_tokens: int, latent: int, hidden: int, eps: float, weigh
 def moe_router_bias_update(plan: c_void_p, expert_offsets: int, num_tokens: int, rate: float,
                            router_b: int, stream: Optional[int] = None) -> None:
     _check(load_library().moe_router_bias_update(plan, expert_offsets, num_tokens, rate, router_b, stream))
+
+
+def moe_quantize_mx4(src: int, src_dtype: int, rows: int, cols: int, ld_src: int, codes: int, scales: int,
+                     stream: Optional[int] = None) -> None:
+    _check(load_library().moe_quantize_mx4(src, src_dtype, rows, cols, ld_src, codes, scales, stream))
+
+
+def moe_dequantize_mx4(codes: int, scales: int, rows: int, cols: int, dst: int, dst_dtype: int, ld_dst: int,
+                       stream: Optional[int] = None) -> None:
+    _check(load_library().moe_dequantize_mx4(codes, scales, rows, cols, dst, dst_dtype, ld_dst, stream))
+
+
+def moe_linear_mx4(a_codes: int, a_scales: int, rows: int, w_codes: int, w_scales: int, mats: int,
+                   offsets: Optional[int], n: int, k: int, y: int, y_dtype: int, ld_y: int,
+                   stream: Optional[int] = None) -> None:
+    _check(load_library().moe_linear_mx4(a_codes, a_scales, rows, w_codes, w_scales, mats, offsets, n, k, y,
+                                         y_dtype, ld_y, stream))
+
+
+def moe_sort_tokens_workspace_bytes(num_tokens: int, top_k: int, num_experts: int) -> int:
+    out = c_size_t()
+    _check(load_library().moe_sort_tokens_workspace_bytes(num_tokens, top_k, num_experts, ctypes.byref(out)))
+    return out.value
+
+
+def moe_sort_tokens(ids: int, id_dtype: int, num_tokens: int, top_k: int, num_experts: int, offsets: int,
+                    row_src: int, token_row: int, workspace: Optional[int], workspace_bytes: int,
+                    stream: Optional[int] = None) -> None:
+    _check(load_library().moe_sort_tokens(ids, id_dtype, num_tokens, top_k, num_experts, offsets, row_src,
+                                          token_row, workspace, workspace_bytes, stream))
+
+
+def moe_dispatch_rows(x: int, row_bytes: int, ld_x: int, token_row: int, num_tokens: int, top_k: int,
+                      num_rows: Optional[int], rows_cap: int, xs: int, ld_xs: int,
+                      stream: Optional[int] = None) -> None:
+    _check(load_library().moe_dispatch_rows(x, row_bytes, ld_x, token_row, num_tokens, top_k, num_rows,
+                                            rows_cap, xs, ld_xs, stream))
+
+
+def moe_combine_rows(rows: int, dtype: int, rows_cap: int, d: int, ld_rows: int, token_row: int,
+                     w: Optional[int], num_tokens: int, top_k: int, y: int, ld_y: int,
+                     stream: Optional[int] = None) -> None:
+    _check(load_library().moe_combine_rows(rows, dtype, rows_cap, d, ld_rows, token_row, w, num_tokens, top_k,
+                                           y, ld_y, stream))
+
+
+def moe_combine_rows_backward(dy: int, rows: Optional[int], dtype: int, rows_cap: int, d: int, ld_dy: int,
+                              ld_rows: int, token_row: int, w: Optional[int], num_tokens: int, top_k: int,
+                              num_rows: Optional[int], drows: Optional[int], ld_drows: int,
+                              dw: Optional[int], stream: Optional[int] = None) -> None:
+    _check(load_library().moe_combine_rows_backward(dy, rows, dtype, rows_cap, d, ld_dy, ld_rows, token_row,
+                                                    w, num_tokens, top_k, num_rows, drows, ld_drows, dw,
+                                                    stream))

@@ -1,0 +1,191 @@
+"""Tokens sorted by expert and back, with gradients (moe_sort_tokens,
+moe_dispatch_rows, moe_combine_rows and moe_combine_rows_backward).
+
+    order = sort_tokens(ids, num_experts)          # ids [T, k] from a router
+    xs = dispatch(x, order)                        # [T*k, d], sorted by expert
+    rows = ...                                     # expert e has rows offsets[e] .. offsets[e+1]-1
+    y = combine(rows, weights, order)              # [T, d]
+
+``dispatch`` and ``combine`` are differentiable (x; rows and weights), once.
+Every call goes to the current stream of its tensors' GPU; nothing is
+synchronised, so all of it can be captured into a graph.  A backward pass that
+is captured needs leaves that no graph built outside the capture still holds
+(autograd would bring that graph's stream into the capture): capture the
+forward pass with it on ``x.detach().requires_grad_()``, or call
+``dispatch_backward`` and ``combine_backward``, which use no autograd.
+"""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import mxmoe as M
+from .layer import check_device, row_dtype, stream_of
+
+
+@dataclass(frozen=True)
+class TokenOrder:
+    """Which row belongs to which (token, choice): see moe_sort_tokens."""
+    offsets: torch.Tensor    # int32 [E+1] first row of each expert; offsets[E] rows in all
+    row_src: torch.Tensor    # int32 [T*k] pair t*k + j of each row, -1 behind the last
+    token_row: torch.Tensor  # int32 [T, k] row of each pair, -1 for a dropped one
+
+    @property
+    def num_experts(self) -> int:
+        return self.offsets.numel() - 1
+
+    @property
+    def num_tokens(self) -> int:
+        return self.token_row.shape[0]
+
+    @property
+    def top_k(self) -> int:
+        return self.token_row.shape[1]
+
+    @property
+    def capacity(self) -> int:
+        """Rows of a buffer that holds every pair."""
+        return self.token_row.numel()
+
+    def _num_rows(self) -> int:
+        return self.offsets.data_ptr() + 4 * self.num_experts
+
+
+def sort_tokens(ids: torch.Tensor, num_experts: int) -> TokenOrder:
+    """The order of the pairs of ``ids`` (int32 or int64 [T, k]) sorted by expert;
+    ids outside [0, num_experts) are dropped (-1: padding)."""
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64 [T, k], got {ids.dtype} with {ids.dim()} dimensions")
+    check_device(ids)
+    ids = ids.contiguous()
+    t, k = ids.shape
+    need = M.moe_sort_tokens_workspace_bytes(t, k, num_experts)
+    i32 = dict(dtype=torch.int32, device=ids.device)
+    offsets, row_src, token_row = torch.empty(num_experts + 1, **i32), torch.empty(t * k, **i32), torch.empty((t, k), **i32)
+    ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+    with torch.cuda.device(ids.device):
+        M.moe_sort_tokens(ids.data_ptr(), M.MOE_ID_INT64 if ids.dtype == torch.int64 else M.MOE_ID_INT32, t, k,
+                          num_experts, offsets.data_ptr(), row_src.data_ptr(), token_row.data_ptr(),
+                          ws.data_ptr() if need else None, need, stream_of(ids))
+    return TokenOrder(offsets, row_src, token_row)
+
+
+def _matrix(x: torch.Tensor, rows: int, what: str) -> torch.Tensor:
+    """x [rows, d] with dense rows that do not overlap (else a copy)."""
+    if x.dim() != 2 or x.shape[0] != rows:
+        raise ValueError(f"{what} must be [{rows}, d], got {tuple(x.shape)}")
+    d = x.shape[1]
+    return x if (d == 0 or x.stride(1) == 1) and (rows < 2 or x.stride(0) >= d) else x.contiguous()
+
+
+def _ld(x: torch.Tensor) -> int:
+    return max(x.stride(0), x.shape[1])
+
+
+def _dispatch(x: torch.Tensor, order: TokenOrder) -> torch.Tensor:
+    x = _matrix(x, order.num_tokens, "x")
+    xs = torch.empty((order.capacity, x.shape[1]), dtype=x.dtype, device=x.device)
+    sz = x.element_size()
+    with torch.cuda.device(x.device):
+        M.moe_dispatch_rows(x.data_ptr(), x.shape[1] * sz, _ld(x) * sz, order.token_row.data_ptr(), order.num_tokens,
+                            order.top_k, order._num_rows(), order.capacity, xs.data_ptr(), xs.shape[1] * sz,
+                            stream_of(x))
+    return xs
+
+
+def _combine(rows: torch.Tensor, weights: Optional[torch.Tensor], order: TokenOrder) -> torch.Tensor:
+    rows = _matrix(rows, order.capacity, "rows")
+    d = rows.shape[1]
+    y = torch.empty((order.num_tokens, d), dtype=rows.dtype, device=rows.device)
+    with torch.cuda.device(rows.device):
+        M.moe_combine_rows(rows.data_ptr(), row_dtype(rows.dtype), order.capacity, d, _ld(rows),
+                           order.token_row.data_ptr(), weights.data_ptr() if weights is not None else None,
+                           order.num_tokens, order.top_k, y.data_ptr(), d, stream_of(rows))
+    return y
+
+
+def dispatch_backward(dxs: torch.Tensor, order: TokenOrder) -> torch.Tensor:
+    """Gradient of :func:`dispatch`: dx [T, d] from dxs [T*k, d]."""
+    row_dtype(dxs.dtype)
+    check_device(dxs, order.token_row)
+    return _combine(dxs, None, order)
+
+
+def combine_backward(dy: torch.Tensor, rows: Optional[torch.Tensor], weights: Optional[torch.Tensor],
+                     order: TokenOrder, need_rows: bool = True, need_weights: bool = True):
+    """Gradients of :func:`combine` from dy [T, d]: (drows [T*k, d] or None, dweights [T, k] or None).
+    ``rows`` is needed for dweights only."""
+    dy = _matrix(dy, order.num_tokens, "dy")
+    dt, d = row_dtype(dy.dtype), dy.shape[1]
+    if need_weights:
+        if rows is None or rows.dtype != dy.dtype or rows.dim() != 2 or rows.shape[1] != d:
+            raise ValueError("the gradient of the weights needs rows of dy's type and width")
+        rows = _matrix(rows, order.capacity, "rows")
+    _check_weights(weights, order)
+    check_device(dy, rows if need_weights else None, weights, order.token_row)
+    weights = weights.contiguous() if weights is not None else None
+    drows = torch.empty((order.capacity, d), dtype=dy.dtype, device=dy.device) if need_rows else None
+    dw = torch.empty(order.token_row.shape, dtype=torch.float32, device=dy.device) if need_weights else None
+    with torch.cuda.device(dy.device):
+        M.moe_combine_rows_backward(
+            dy.data_ptr(), rows.data_ptr() if need_weights else None, dt, order.capacity, d, _ld(dy),
+            _ld(rows) if need_weights else d, order.token_row.data_ptr(),
+            weights.data_ptr() if weights is not None else None, order.num_tokens, order.top_k, order._num_rows(),
+            drows.data_ptr() if need_rows else None, d, dw.data_ptr() if need_weights else None, stream_of(dy))
+    return drows, dw
+
+
+def _check_weights(weights: Optional[torch.Tensor], order: TokenOrder) -> None:
+    if weights is not None and (weights.dtype != torch.float32 or weights.shape != order.token_row.shape):
+        raise ValueError(f"weights must be float32 {list(order.token_row.shape)}, got {weights.dtype} {list(weights.shape)}")
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, order):
+        ctx.order = order
+        return _dispatch(x, order)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dxs):
+        return _combine(dxs, None, ctx.order), None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weights, order):
+        need_w = weights is not None and weights.requires_grad
+        ctx.order = order
+        ctx.save_for_backward(rows if need_w else None, weights)
+        return _combine(rows, weights.contiguous() if weights is not None else None, order)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        rows, weights = ctx.saved_tensors
+        need_rows, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        return (*combine_backward(dy, rows, weights, ctx.order, need_rows, need_w), None)
+
+
+def dispatch(x: torch.Tensor, order: TokenOrder) -> torch.Tensor:
+    """xs [T*k, d]: row r is the row of x of the token that ``order.row_src[r]`` belongs to; zeros behind
+    the last row.  Any element type moves (MXFP4 codes and scales too); bf16, fp16 and fp32 have a gradient,
+    dx[t] = sum of its rows' gradients in fp32."""
+    check_device(x, order.token_row)
+    if x.requires_grad:
+        row_dtype(x.dtype)
+    return _Dispatch.apply(x, order)
+
+
+def combine(rows: torch.Tensor, weights: Optional[torch.Tensor], order: TokenOrder) -> torch.Tensor:
+    """y [T, d]: the sum of a token's rows [T*k, d] (bf16, fp16 or fp32) times their float32 weights [T, k]
+    (None: ones), in fp32, rounded once; a token whose pairs are all dropped gets zeros."""
+    row_dtype(rows.dtype)
+    _check_weights(weights, order)
+    check_device(rows, weights, order.token_row)
+    return _Combine.apply(rows, weights, order)
