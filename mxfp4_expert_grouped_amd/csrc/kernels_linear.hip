@@ -51,8 +51,8 @@ __device__ __forceinline__ void mat_rows(const LinearArgs& a, int e, int& lo, in
   hi = max(lo, min(max(a.offsets[e + 1], 0), rows));
 }
 
-// prefix[e] = row tiles (of TM rows) of the matrices before e, for e <= mats;
-// one pass of the whole workgroup.  Returns the number of tiles.
+// prefix[e] = row tiles (of TM rows) of the matrices before e; one pass of the
+// whole workgroup (part: a word of LDS per wave).  Returns the number of tiles.
 template <int THREADS, int TM>
 __device__ __forceinline__ int tile_prefix(const LinearArgs& a, int* prefix, int* part) {
   constexpr int PER = kMaxMats / THREADS;
@@ -84,10 +84,9 @@ __device__ __forceinline__ int tile_prefix(const LinearArgs& a, int* prefix, int
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = tid * PER + i;
-    if (e <= a.mats && e < kMaxMats) prefix[e] = at;
+    if (e < a.mats) prefix[e] = at;
     at += n[i];
   }
-  if (tid == 0) prefix[a.mats] = total;
   __syncthreads();
   return total;
 }
@@ -137,7 +136,7 @@ constexpr int kStreamThreads = 256, kStreamWaves = kStreamThreads / 64;
 
 template <typename T, int SCALES>
 __global__ void __launch_bounds__(kStreamThreads, 4) k_linear_stream(LinearArgs a, bool wide) {
-  __shared__ int prefix[kMaxMats + 1];
+  __shared__ int prefix[kMaxMats];
   __shared__ int part[kStreamWaves];
   __shared__ float4 sums[kStreamWaves][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -209,34 +208,38 @@ __global__ void __launch_bounds__(kStreamThreads, 4) k_linear_stream(LinearArgs 
 
 // ---------------------------------------------------------------------------
 // Many rows per matrix: BM x 256 tiles through LDS.  One workgroup of four
-// waves per CU walks its tiles; a step is 128 of K.  The step's codes (64
-// bytes of each of BM activation and 256 weight rows) come by direct-to-LDS
-// copies into a ring of S slots, and the stream of steps runs on across the
-// tiles: while a tile ends, the first steps of the next are already on their
-// way.  Per step a wave issues
-//   16 MI NI / 16 MFMAs 32x32x64 of K half 0, between them the LDS reads of
-//   half 1; then, with its own copies of step s + 1 landed and a barrier (all
-//   waves' copies have landed, and all have read slot s), those of half 1,
-//   between them the reads of half 0 of step s + 1 and the copies of step
-//   s + S into slot s.
+// waves per CU walks its tiles; a step is 256 of K, four quarters of 64.  The
+// step's codes (128 bytes of each of BM activation and 256 weight rows) come
+// by direct-to-LDS copies into a ring of S slots, and the stream of steps runs
+// on across the tiles: while a tile ends, the first steps of the next are
+// already on their way.  In a quarter a wave issues its MI x NI MFMAs
+// 32x32x64 and between them the LDS reads of the next quarter; before the last
+// quarter it waits for its own copies of step s + 1 and at a barrier (all
+// waves' copies have landed, and all have read slot s), and from there on the
+// copies of step s + S go into slot s, spread over the following quarters so
+// that the waves do not queue behind them.
 // The weights are the first MFMA operand: lane (l32, g32) register r of a
 // 32x32 result is column 8(r/4) + 4 g32 + r%4 of activation row l32, so four
 // registers are four consecutive columns of y.
 //
-// LDS slot: activation rows, then weight rows, 64 bytes each; the 16-byte
-// chunk c of row r sits at chunk c ^ ((r/4) % 4), so that the eight lanes that
-// the LDS serves together (eight rows, one chunk) touch all banks once.  A copy
-// moves 16 rows: lane l brings chunk (l%4) ^ (l/16) of row l/4, four lanes the
-// 64 bytes of a row.
+// LDS slot: activation rows, then weight rows, 128 bytes each; the 16-byte
+// chunk c of row r sits at chunk c ^ (r%8), so that the eight lanes that the
+// LDS serves together (eight rows, one chunk) touch all banks once.  A copy
+// moves 8 rows: lane l brings chunk (l%8) ^ (l/8) of row l/8, eight lanes the
+// 128 bytes (one cache line) of a row.  Pieces of 64 bytes, from steps half as
+// wide, cost a quarter of the copies' rate: 95 against 75 us for the copies
+// alone of 8192 x 4096 x 7168.
 //
 // Scales.  AG (k % 512 == 0, scale rows on 16 bytes): one 16-byte piece per
-// row holds four steps' scales, copied every fourth step into one of two
-// buffers and kept in registers for those steps.  Otherwise a dword per row
-// and step, in the slot.  Byte 2h + g32 of a step's dword belongs to K half h
-// of lane (l32, g32): shifted by 8 g32 once per step, the MFMA takes byte 2h.
+// row holds two steps' scales, copied every second step into one of two
+// buffers and kept in registers for those steps.  Otherwise two dwords per row
+// and step, in the slot.  A dword holds half a step's scales, byte 2q + g32
+// that of its quarter q of lane (l32, g32): shifted by 8 g32 once per step,
+// the MFMA takes byte 2q.
 //
-// Rows past the tile's or the matrix's end are copied from the last valid row
-// and their results not stored.
+// With k % 256 == 128 a row's last step is half a step: its copies bring the
+// first 64 bytes twice, and it has two quarters.  Rows past the tile's or the
+// matrix's end are copied from the last valid row and their results not stored.
 // ---------------------------------------------------------------------------
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -304,37 +307,43 @@ constexpr int kTileN = 256, kTileThreads = 256;
 constexpr int kMaxTiles = 1 << 30;
 constexpr int kPanel = 4;  // row tiles that share a column block's weights in time
 
-template <int BM, bool AG>
+template <int SZ, int BM, bool AG>
 struct TileShape {
   static constexpr int WM = BM == 64 ? 1 : 2, WN = 4 / WM;        // waves along rows, columns
   static constexpr int MI = BM / WM / 32, NI = kTileN / WN / 32;  // 32-row, 32-column blocks of a wave
-  static constexpr int S = BM == 256 ? 4 : BM == 128 ? 5 : 7;     // ring slots
-  static constexpr int A = 0, W = BM * 64, SC = W + kTileN * 64;  // slot: activations, weights, scale dwords
-  static constexpr int SLOT = SC + (AG ? 0 : (BM + kTileN) * 4);
+  static constexpr int S = BM == 256 ? 2 : 3;                     // ring slots
+  static constexpr int A = 0, W = BM * 128, SC = W + kTileN * 128;  // slot: activations, weights, scale dwords
+  static constexpr int SLOT = SC + (AG ? 0 : (BM + kTileN) * 8);
   static constexpr int GROUP = S * SLOT;                          // scale pieces of AG, two buffers
   static constexpr int LDS = GROUP + (AG ? 2 * (BM + kTileN) * 16 : 0);
-  static constexpr int CA = BM / 64, CW = 4;                      // copies of codes per wave and step
-  // copies of a wave for a step that is the I-th of its group
-  static constexpr int copies(int i) { return CA + CW + (AG ? (i % 4 == 0 ? 2 : 0) : 2); }
+  static constexpr int CA = BM / 32, CW = 8;                      // copies of codes per wave and step
+  // copies of a wave for a step, the first (i even) or second of its pair
+  static constexpr int copies(int i) { return CA + CW + (AG ? (i % 2 == 0 ? 2 : 0) : 4); }
+  static constexpr int copies_from(int i, int n) { return n <= 0 ? 0 : copies(i) + copies_from(i + 1, n - 1); }
+  // those issued in the last quarter before their step's slot is S - 1 steps
+  // away: half of them with two slots (they have to land soon), else a quarter
+  static constexpr int first_part(int i) { return copies(i) / (S == 2 ? 2 : 4); }
+  static constexpr int STORES = MI * NI * 4 * SZ / 4;             // a wave's stores of a tile (16 bytes a lane)
 };
 
 // WIDE: n and the rows of y are whole numbers of 16-byte pieces.
 template <typename T, int BM, bool AG, bool WIDE>
 __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
-  using P = TileShape<BM, AG>;
+  using P = TileShape<sizeof(T), BM, AG>;
   constexpr int S = P::S, MI = P::MI, NI = P::NI, NM = MI * NI;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[P::LDS];
-  __shared__ int prefix[kMaxMats + 1];
-  __shared__ int part[kTileThreads / 64];
+  __shared__ int prefix[kMaxMats];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int l32 = lane & 31, g32 = lane >> 5;
   const int wm = wave / P::WN, wn = wave % P::WN;
-  const int mtiles = __builtin_amdgcn_readfirstlane(tile_prefix<kTileThreads, BM>(a, prefix, part));
+  const int mtiles =
+      __builtin_amdgcn_readfirstlane(tile_prefix<kTileThreads, BM>(a, prefix, reinterpret_cast<int*>(lds)));
   const int ntn = (a.n + kTileN - 1) / kTileN;
   // (rows / BM + mats row tiles of at most 4096 column blocks stay below the
   // limit; only ranges that overlap could have more)
   const int total = min(mtiles, kMaxTiles / ntn) * ntn;
-  const int nsteps = a.k / 128;
+  const int nsteps = (a.k + 255) / 256;
+  const bool odd = !AG && (a.k & 128);  // the last step is half a step
 
   // ---- which tiles are this workgroup's: runs of gridDim/8 consecutive
   // tiles go to one XCD (workgroups go to the XCDs round-robin), so that the
@@ -353,7 +362,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     const int q = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(ntn)));
     TileAt t;
     t.e = tile_matrix(prefix, a.mats, q);
-    const int p0 = __builtin_amdgcn_readfirstlane(prefix[t.e]), p1 = __builtin_amdgcn_readfirstlane(prefix[t.e + 1]);
+    const int p0 = __builtin_amdgcn_readfirstlane(prefix[t.e]);
+    const int p1 = t.e + 1 < a.mats ? __builtin_amdgcn_readfirstlane(prefix[t.e + 1]) : mtiles;
     const uint32_t local = pos - p0 * ntn, pn = kPanel * ntn;
     const int panel = __builtin_amdgcn_readfirstlane(static_cast<int>(local / pn)), within = local - panel * pn;
     const int gm = min(kPanel, p1 - p0 - panel * kPanel);
@@ -377,7 +387,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   const uint8_t *ia = nullptr, *iw = nullptr, *ias = nullptr, *iws = nullptr;  // the tile's first row, column
   uint32_t oa[P::CA], ow[P::CW], osa, osw;
   const int kb = a.k / 2, sb = a.k / 32;
-  const int sa_blk = wave % P::CA;  // 64-row block of activation scales that this wave copies
+  const int sa_blk = wave % (BM / 64);  // 64-row block of activation scales that this wave copies
+  // half a step's copies: chunks 4-7 are not there, the first four come again
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const uint32_t half_back = chunk & 4 ? 64 : 0;
   auto iss_setup = [&](const TileAt& t) {
     ia = uniform(a.a_c + int64_t(t.row0) * kb);
     ias = uniform(a.a_s + int64_t(t.row0) * sb);
@@ -385,30 +398,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     iw = uniform(a.w_c + wrow * kb);
     iws = uniform(a.w_s + wrow * sb);
     const int rlast = t.rows - 1, clast = min(kTileN, a.n - t.col0) - 1;
-    const int chunk = 16 * ((lane & 3) ^ (lane >> 4));
 #pragma unroll
-    for (int q = 0; q < P::CA; ++q) oa[q] = min(16 * (P::CA * wave + q) + (lane >> 2), rlast) * kb + chunk;
+    for (int q = 0; q < P::CA; ++q) oa[q] = min(8 * (P::CA * wave + q) + (lane >> 3), rlast) * kb + 16 * chunk;
 #pragma unroll
-    for (int q = 0; q < P::CW; ++q) ow[q] = min(16 * (P::CW * wave + q) + (lane >> 2), clast) * kb + chunk;
+    for (int q = 0; q < P::CW; ++q) ow[q] = min(8 * (P::CW * wave + q) + (lane >> 3), clast) * kb + 16 * chunk;
     osa = min(64 * sa_blk + lane, rlast) * sb;
     osw = min(64 * wave + lane, clast) * sb;
   };
   // (total and G are at most 2^30: no overflow)
   auto next_pos = [&](int pos) { return pos + G; };
-  // The copies of the step at the issue side, numbered 0 .. copies-1; I: its
-  // place in its group of four steps.
+  // Copy number m of the step at the issue side, the I-th of its pair.
   auto issue = [&](auto ic, auto mc) {
-    constexpr int I = decltype(ic)::value, m = decltype(mc)::value;
+    constexpr int I = decltype(ic)::value, m = decltype(mc)::value, n = m - P::CA - P::CW;
     const uint32_t slot = lds0 + iss_slot * P::SLOT;
-    if constexpr (m < P::CA) copy16(oa[m], ia, slot + P::A + (P::CA * wave + m) * 1024);
-    else if constexpr (m < P::CA + P::CW) copy16(ow[m - P::CA], iw, slot + P::W + (P::CW * wave + m - P::CA) * 1024);
+    const bool half = odd && iss_step == nsteps - 1;
+    const uint32_t back = half ? half_back : 0;
+    if constexpr (m < P::CA) copy16(oa[m] - back, ia, slot + P::A + (P::CA * wave + m) * 1024);
+    else if constexpr (n < 0) copy16(ow[m - P::CA] - back, iw, slot + P::W + (P::CW * wave + m - P::CA) * 1024);
     else if constexpr (!AG) {
-      if constexpr (m == P::CA + P::CW) copy4(osa, ias, slot + P::SC + sa_blk * 256);
-      if constexpr (m == P::CA + P::CW + 1) copy4(osw, iws, slot + P::SC + BM * 4 + wave * 256);
+      // dword n/2 of the step (half a step has one: it comes again)
+      const uint32_t d = n >= 2 && !half ? 4 : 0;
+      if constexpr (n % 2 == 0) copy4(osa + d, ias, slot + P::SC + (n / 2) * (BM + kTileN) * 4 + sa_blk * 256);
+      else copy4(osw + d, iws, slot + P::SC + (n / 2) * (BM + kTileN) * 4 + BM * 4 + wave * 256);
     } else if constexpr (I == 0) {
       const uint32_t buf = lds0 + P::GROUP + iss_group * (BM + kTileN) * 16;
-      if constexpr (m == P::CA + P::CW) copy16(osa, ias, buf + sa_blk * 1024);
-      if constexpr (m == P::CA + P::CW + 1) copy16(osw, iws, buf + BM * 16 + wave * 1024);
+      if constexpr (n == 0) copy16(osa, ias, buf + sa_blk * 1024);
+      else copy16(osw, iws, buf + BM * 16 + wave * 1024);
     }
   };
   // to the next step; behind the last tile the last one is copied again, into
@@ -416,41 +431,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   auto advance = [&](auto ic) {
     constexpr int I = decltype(ic)::value;
     iss_slot = iss_slot + 1 == S ? 0 : iss_slot + 1;
-    ia += 64;
-    iw += 64;
+    ia += 128;
+    iw += 128;
     if (!AG) {
-      ias += 4;
-      iws += 4;
-    } else if (I == 3) {
+      ias += 8;
+      iws += 8;
+    } else if (I == 1) {
       ias += 16;
       iws += 16;
       iss_group ^= 1;
     }
     ++iss_step;
-    // (with AG a tile ends with a group of four steps)
-    if ((!AG || I == 3) && iss_step == nsteps) {
+    // (with AG a tile ends with a pair of steps)
+    if ((!AG || I == 1) && iss_step == nsteps) {
       iss_step = 0;
       if (next_pos(iss_pos) < total) iss_pos = next_pos(iss_pos);
       iss_setup(tile_at(iss_pos));
     }
   };
 
-  // ---- read side: byte offsets in a slot of this lane's fragments of K half
-  // 0 (half 1: chunk ^ 2), row blocks 2048 bytes apart
-  const int swz = (l32 >> 2) & 3;
-  const int fa = P::A + (wm * MI * 32 + l32) * 64, fw = P::W + (wn * NI * 32 + l32) * 64;
-  const int ch[2] = {16 * (g32 ^ swz), 16 * ((2 + g32) ^ swz)};
-  uint4 av[2][MI], wv[2][NI];
-  uint4 agr[MI], wgr[NI];           // AG: four steps' scales
-  uint32_t araw[MI], wraw[NI];      // otherwise the next step's
-  uint32_t asc[MI], wsc[NI];
+  // ---- read side: byte offsets in a slot of this lane's fragments, row
+  // blocks 4096 bytes apart; quarter h of a step is chunks 2h and 2h + 1
+  const int fa = P::A + (wm * MI * 32 + l32) * 128, fw = P::W + (wn * NI * 32 + l32) * 128;
+  const int ch[4] = {16 * (g32 ^ (l32 & 7)), 16 * ((2 + g32) ^ (l32 & 7)), 16 * ((4 + g32) ^ (l32 & 7)),
+                     16 * ((6 + g32) ^ (l32 & 7))};
+  uint4 av[2][MI], wv[2][NI];       // the fragments of this quarter and of the next
+  uint4 agr[MI], wgr[NI];           // AG: two steps' scales
+  uint2 araw[MI], wraw[NI];         // otherwise the next step's
+  uint32_t asc[2][MI], wsc[2][NI];  // this step's, of its first and second half
   auto read_frag = [&](int slot, auto hc, auto jc) {
     constexpr int H = decltype(hc)::value, j = decltype(jc)::value;
     const uint8_t* p = lds + slot * P::SLOT;
-    if constexpr (j < NI) wv[H][j] = *reinterpret_cast<const uint4*>(p + fw + ch[H] + j * 2048);
-    else av[H][j - NI] = *reinterpret_cast<const uint4*>(p + fa + ch[H] + (j - NI) * 2048);
+    if constexpr (j < NI) wv[H % 2][j] = *reinterpret_cast<const uint4*>(p + fw + ch[H] + j * 4096);
+    else av[H % 2][j - NI] = *reinterpret_cast<const uint4*>(p + fa + ch[H] + (j - NI) * 4096);
   };
-  // scales of the step in `slot`, the I-th of its group (group buffer grp)
+  // scales of the step in `slot`, the I-th of its pair (scale buffer grp)
   auto read_scales = [&](int slot, int grp, auto ic) {
     constexpr int I = decltype(ic)::value;
     if constexpr (AG) {
@@ -462,22 +477,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
         for (int i = 0; i < MI; ++i) agr[i] = *reinterpret_cast<const uint4*>(p + ((wm * MI + i) * 32 + l32) * 16);
       }
     } else {
-      const uint8_t* p = lds + slot * P::SLOT + P::SC;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(lds + slot * P::SLOT + P::SC);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) wraw[j] = *reinterpret_cast<const uint32_t*>(p + (BM + (wn * NI + j) * 32 + l32) * 4);
+      for (int j = 0; j < NI; ++j) {
+        const int at = BM + (wn * NI + j) * 32 + l32;
+        wraw[j] = make_uint2(p[at], p[at + BM + kTileN]);
+      }
 #pragma unroll
-      for (int i = 0; i < MI; ++i) araw[i] = *reinterpret_cast<const uint32_t*>(p + ((wm * MI + i) * 32 + l32) * 4);
+      for (int i = 0; i < MI; ++i) {
+        const int at = (wm * MI + i) * 32 + l32;
+        araw[i] = make_uint2(p[at], p[at + BM + kTileN]);
+      }
     }
   };
   auto shift_scales = [&](auto ic) {
     constexpr int I = decltype(ic)::value;
-    auto pick = [&](const uint4& g, uint32_t raw) -> uint32_t {
-      return (AG ? (I == 0 ? g.x : I == 1 ? g.y : I == 2 ? g.z : g.w) : raw) >> (8 * g32);
-    };
+    const int sh = 8 * g32;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) wsc[j] = pick(wgr[j], wraw[j]);
+    for (int j = 0; j < NI; ++j) {
+      wsc[0][j] = (AG ? (I == 0 ? wgr[j].x : wgr[j].z) : wraw[j].x) >> sh;
+      wsc[1][j] = (AG ? (I == 0 ? wgr[j].y : wgr[j].w) : wraw[j].y) >> sh;
+    }
 #pragma unroll
-    for (int i = 0; i < MI; ++i) asc[i] = pick(agr[i], araw[i]);
+    for (int i = 0; i < MI; ++i) {
+      asc[0][i] = (AG ? (I == 0 ? agr[i].x : agr[i].z) : araw[i].x) >> sh;
+      asc[1][i] = (AG ? (I == 0 ? agr[i].y : agr[i].w) : araw[i].y) >> sh;
+    }
   };
 
   v16f acc[MI][NI];
@@ -490,48 +515,59 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
       for (int j = 0; j < NI; ++j) asm volatile("" : "+a"(acc[i][j]));
   };
   int slot = 0, group = 0;
-  // One step.  after_stores: the last tile's stores are among the
-  // outstanding operations, so the wait takes them all.
-  auto step = [&](auto ic, bool after_stores) {
-    constexpr int I = decltype(ic)::value;
+  // One step, the I-th of its pair, of NQ quarters (4, or 2 for half a step).
+  // FIRST: the tile's first, its products start from zero.  after_stores: the
+  // last tile's stores may still be on their way (operations finish in the
+  // order in which they were issued).
+  auto step = [&](auto ic, auto nq, auto first_c, bool after_stores) {
+    constexpr int I = decltype(ic)::value, NQ = decltype(nq)::value;
+    constexpr bool FIRST = decltype(first_c)::value != 0;
     const int nslot = slot + 1 == S ? 0 : slot + 1;
     shift_scales(ic);
-    unrolled<0, NM>([&](auto kc) {
-      constexpr int k = decltype(kc)::value, i = k / NI, j = k % NI;
-      acc[i][j] = mfma32_fp4<0>(wv[0][j], av[0][i], acc[i][j], wsc[j], asc[i]);
-      // the reads of half 1, spread over the first three quarters
-      constexpr int R = MI + NI, lo = k * R / (NM * 3 / 4), hi = (k + 1) * R / (NM * 3 / 4);
-      unrolled<(lo < R ? lo : R), (hi < R ? hi : R)>([&](auto jc) { read_frag(slot, Int<1>{}, jc); });
-      __builtin_amdgcn_sched_barrier(0);
+    // the copies of step s + S - 1, begun in the last quarter of step s - 1,
+    // go on over the quarters before the barrier (with two slots: the first)
+    constexpr int IP = (I + S - 1) % 2, CP = P::copies(IP), C0 = P::first_part(IP);
+    constexpr int QI = S == 2 ? 1 : NQ - 1;  // quarters that issue them
+    unrolled<0, NQ>([&](auto qc) {
+      constexpr int q = decltype(qc)::value;
+      constexpr bool LAST = q == NQ - 1;
+      if constexpr (q == QI || (LAST && QI > NQ - 1)) {
+        settle();
+        advance(Int<IP>{});
+      }
+      if constexpr (LAST) {
+        settle();
+        wait_lds();
+        // outstanding: the copies of steps s + 1 .. s + S - 1, of which
+        // s + 1's have to be done (with more than two slots all of them were
+        // issued before the stores)
+        constexpr int left = P::copies_from(I + 2, S - 2);
+        if (S > 2 && after_stores) wait_vm<(left + P::STORES < 63 ? left + P::STORES : 63)>();
+        else wait_vm<left>();
+        tile_barrier();
+      }
+      unrolled<0, NM>([&](auto kc) {
+        constexpr int k = decltype(kc)::value, i = k / NI, j = k % NI;
+        acc[i][j] = mfma32_fp4<q % 2>(wv[q % 2][j], av[q % 2][i], FIRST && q == 0 ? v16f{} : acc[i][j], wsc[q / 2][j], asc[q / 2][i]);
+        if constexpr (LAST && k == 0) read_scales(nslot, I == 1 ? group ^ 1 : group, Int<(I + 1) % 2>{});
+        // the next quarter's reads, in the first three quarters of this one
+        constexpr int R = MI + NI, lo = k * R / (NM * 3 / 4), hi = (k + 1) * R / (NM * 3 / 4);
+        unrolled<(lo < R ? lo : R), (hi < R ? hi : R)>(
+            [&](auto jc) { read_frag(LAST ? nslot : slot, Int<LAST ? 0 : q + 1>{}, jc); });
+        if constexpr (q < QI) {
+          constexpr int n = NM * QI, x = q * NM + k;
+          unrolled<C0 + x * (CP - C0) / n, C0 + (x + 1) * (CP - C0) / n>([&](auto mc) { issue(Int<IP>{}, mc); });
+        }
+        if constexpr (LAST) {
+          constexpr int C = P::first_part(I + S);
+          unrolled<k * C / NM, (k + 1) * C / NM>([&](auto mc) { issue(Int<(I + S) % 2>{}, mc); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
     });
     settle();
-    wait_lds();
-    // outstanding: the copies of steps s + 1 .. s + S - 1, of which s + 1's
-    // have to be done
-    constexpr int left = [] {
-      int n = 0;
-      for (int q = 2; q < S; ++q) n += P::copies(I + q);
-      return n;
-    }();
-    if (after_stores) wait_vm<0>();
-    else wait_vm<left>();
-    tile_barrier();
-    constexpr int C = P::copies(I + S);
-    unrolled<0, NM>([&](auto kc) {
-      constexpr int k = decltype(kc)::value, i = k / NI, j = k % NI;
-      acc[i][j] = mfma32_fp4<1>(wv[1][j], av[1][i], acc[i][j], wsc[j], asc[i]);
-      if constexpr (k == 0) read_scales(nslot, I == 3 ? group ^ 1 : group, Int<(I + 1) % 4>{});
-      constexpr int R = MI + NI, H = NM / 2;
-      unrolled<(k < H ? k * R / H : R), (k < H ? (k + 1) * R / H : R)>([&](auto jc) { read_frag(nslot, Int<0>{}, jc); });
-      // the copies of step s + S, in the later half
-      unrolled<(k < H ? 0 : (k - H) * C / (NM - H)), (k < H ? 0 : (k - H + 1) * C / (NM - H))>(
-          [&](auto mc) { issue(Int<(I + S) % 4>{}, mc); });
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    settle();
-    advance(Int<(I + S) % 4>{});
     slot = nslot;
-    if (I == 3) group ^= 1;
+    if (I == 1) group ^= 1;
   };
 
   // ---- results: acc[i][j] of this wave.  Buffer stores with the tile's first
@@ -595,27 +631,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     });
   };
 
-  // ---- the stream of steps
+  // ---- the stream of steps: the first S - 1 and the first part of the next
+  // are on their way before the first product
   iss_setup(tile_at(iss_pos));
-  if constexpr (AG) {
-    // a matrix has at least four steps, and S of them start here
-    unrolled<0, S>([&](auto sc) {
-      constexpr int I = decltype(sc)::value % 4;
-      unrolled<0, P::copies(I)>([&](auto mc) { issue(Int<I>{}, mc); });
-      advance(Int<I>{});
-    });
-  } else {
-    for (int q = 0; q < S; ++q) {
-      unrolled<0, P::copies(0)>([&](auto mc) { issue(Int<0>{}, mc); });
-      advance(Int<0>{});
-    }
-  }
-  constexpr int ahead = [] {
-    int n = 0;
-    for (int q = 1; q < S; ++q) n += P::copies(q);
-    return n;
-  }();
-  wait_vm<ahead>();
+  unrolled<0, S - 1>([&](auto sc) {
+    constexpr int I = decltype(sc)::value % 2;
+    unrolled<0, P::copies(I)>([&](auto mc) { issue(Int<I>{}, mc); });
+    advance(Int<I>{});
+  });
+  unrolled<0, P::first_part(S - 1)>([&](auto mc) { issue(Int<(S - 1) % 2>{}, mc); });
+  wait_vm<P::copies_from(1, S - 2) + P::first_part(S - 1)>();
   tile_barrier();
   read_scales(0, 0, Int<0>{});
   unrolled<0, MI + NI>([&](auto jc) { read_frag(0, Int<0>{}, jc); });
@@ -623,25 +648,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   bool stored = false;
   for (int pos = first; pos < total; pos = next_pos(pos)) {
     const TileAt t = tile_at(pos);
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = v16f{};
+    // a store that did not go by 16-byte pieces is not counted: wait for it
+    if (!WIDE && stored) wait_vm<0>();
+    stored &= WIDE;
     if constexpr (AG) {
-      int s = 0;
-      do {
-        step(Int<0>{}, stored);
-        stored = false;
-        step(Int<1>{}, false);
-        step(Int<2>{}, false);
-        step(Int<3>{}, false);
-      } while ((s += 4) < nsteps);
+      step(Int<0>{}, Int<4>{}, Int<1>{}, stored);
+      step(Int<1>{}, Int<4>{}, Int<0>{}, false);
+      for (int s = 2; s < nsteps; s += 2) {
+        step(Int<0>{}, Int<4>{}, Int<0>{}, false);
+        step(Int<1>{}, Int<4>{}, Int<0>{}, false);
+      }
     } else {
-      int s = 0;
-      do {
-        step(Int<0>{}, stored);
-        stored = false;
-      } while (++s < nsteps);
+      // half a step, if there is one, comes last; alone it is the first too
+      if (nsteps == 1 && odd) {
+        step(Int<0>{}, Int<2>{}, Int<1>{}, stored);
+      } else {
+        step(Int<0>{}, Int<4>{}, Int<1>{}, stored);
+        const int full = odd ? nsteps - 1 : nsteps;
+        for (int s = 1; s < full; ++s) step(Int<0>{}, Int<4>{}, Int<0>{}, false);
+        if (odd) step(Int<0>{}, Int<2>{}, Int<0>{}, false);
+      }
     }
     store_tile(t);
     stored = true;
@@ -669,17 +695,21 @@ hipError_t stream_t(const LinearArgs& a, hipStream_t st) {
 
 template <typename T, int BM>
 hipError_t tile_t(const LinearArgs& a, hipStream_t st) {
+  const int64_t sb = a.k / 32;
+  const bool wide = rows_aligned(a.y, a.ld_y * sizeof(T), 16) && a.n % (16 / sizeof(T)) == 0;
+  // (single-element stores and 256 rows need more registers than there are)
+  if constexpr (BM == 256)
+    if (!wide) return tile_t<T, 128>(a, st);
   const int64_t mtiles = a.offsets ? std::min<int64_t>(a.rows, (a.rows + BM - 1) / BM + a.mats) : (a.rows + BM - 1) / BM;
   const int64_t tiles = mtiles * ((a.n + kTileN - 1) / kTileN);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, a.num_cus));
-  const int64_t sb = a.k / 32;
-  const bool wide = rows_aligned(a.y, a.ld_y * sizeof(T), 16) && a.n % (16 / sizeof(T)) == 0;
-  if (!wide)
-    k_linear_tile<T, BM, false, false><<<grid, kTileThreads, 0, st>>>(a);
-  else if (a.k % 512 == 0 && rows_aligned(a.a_s, sb, 16) && rows_aligned(a.w_s, sb, 16))
+  if (!wide) {
+    if constexpr (BM != 256) k_linear_tile<T, BM, false, false><<<grid, kTileThreads, 0, st>>>(a);
+  } else if (a.k % 512 == 0 && rows_aligned(a.a_s, sb, 16) && rows_aligned(a.w_s, sb, 16)) {
     k_linear_tile<T, BM, true, true><<<grid, kTileThreads, 0, st>>>(a);
-  else
+  } else {
     k_linear_tile<T, BM, false, true><<<grid, kTileThreads, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -99,36 +99,48 @@ ROW_DTYPES = {torch.bfloat16: M.MOE_SRC_BF16, torch.float32: M.MOE_SRC_FP32, tor
 
 
 def row_dtype(dtype: torch.dtype) -> int:
-    if dtype not in ROW_DTYPES:
+    dt = ROW_DTYPES.get(dtype)
+    if dt is None:
         raise ValueError(f"expected bfloat16, float16 or float32, got {dtype}")
-    return ROW_DTYPES[dtype]
+    return dt
 
 
-def check_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    """Every tensor on one GPU (the launches go to its current stream)."""
-    if first.device.type != "cuda":
+def device_index(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The GPU that every tensor is on (a call's launches go to its current stream)."""
+    if not first.is_cuda:
         raise ValueError(f"expected tensors on a GPU, got one on {first.device}")
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and (t.get_device() != index or not t.is_cuda):
             raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return index
 
 
-def stream_of(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+def on_device(index: int, call, *args) -> None:
+    """call(*args, stream) with GPU ``index`` current and its current stream.  A few
+    small calls are bound by the host: the device is switched only if it has to be."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        call(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            call(*args, stream)
 
 
 def _mx4_operand(codes: torch.Tensor, scales: torch.Tensor, what: str, dims: int):
     """Contiguous canonical codes [..., K/2] and scales [..., K/32]; -> (codes, scales, K)"""
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise ValueError(f"{what}: codes and scales must be uint8")
-    if codes.dim() != dims or scales.dim() != dims or codes.shape[:-1] != scales.shape[:-1] \
-            or codes.shape[-1] != 16 * scales.shape[-1]:
-        raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not "
-                         "[..., K/2] and [..., K/32]")
-    codes, scales = codes.contiguous(), scales.contiguous()
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != dims or len(ss) != dims or cs[:-1] != ss[:-1] or cs[-1] != 16 * ss[-1]:
+        raise ValueError(f"{what}: codes {tuple(cs)} and scales {tuple(ss)} are not [..., K/2] and [..., K/32]")
+    if not codes.is_contiguous():
+        codes = codes.contiguous()
+    if not scales.is_contiguous():
+        scales = scales.contiguous()
     if codes.data_ptr() % 16:
         codes = codes.clone()
-    return codes, scales, 32 * scales.shape[-1]
+    return codes, scales, 32 * ss[-1]
 
 
 def quantize_mx4(src: torch.Tensor):
@@ -138,30 +150,29 @@ def quantize_mx4(src: torch.Tensor):
     if src.dim() != 2:
         raise ValueError(f"expected a matrix, got {src.dim()} dimensions")
     dt = row_dtype(src.dtype)
-    check_device(src)
+    dev = device_index(src)
     rows, cols = src.shape
     if cols % 32:
         raise ValueError(f"columns ({cols}) must be a multiple of 32")
-    if cols and (src.stride(1) != 1 or src.stride(0) < cols):
+    ld, step = src.stride()
+    if cols and (step != 1 or ld < cols):
         src = src.contiguous()
+        ld = cols
     codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=src.device)
     scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=src.device)
-    with torch.cuda.device(src.device):
-        M.moe_quantize_mx4(src.data_ptr(), dt, rows, cols, max(src.stride(0), cols), codes.data_ptr(),
-                           scales.data_ptr(), stream_of(src))
+    on_device(dev, M.moe_quantize_mx4, src.data_ptr(), dt, rows, cols, max(ld, cols), codes.data_ptr(),
+              scales.data_ptr())
     return codes, scales
 
 
 def dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values of a canonical MXFP4 matrix [rows, K/2], [rows, K/32] (moe_dequantize_mx4)."""
     dt = row_dtype(dtype)
-    check_device(codes, scales)
+    dev = device_index(codes, scales)
     codes, scales, cols = _mx4_operand(codes, scales, "matrix", 2)
     rows = codes.shape[0]
     out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
-    with torch.cuda.device(codes.device):
-        M.moe_dequantize_mx4(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dt, cols,
-                             stream_of(codes))
+    on_device(dev, M.moe_dequantize_mx4, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dt, cols)
     return out
 
 
@@ -177,22 +188,26 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
     No gradient: the product is for inference.
     """
     grouped = offsets is not None
-    check_device(codes, scales, w_codes, w_scales, offsets, out)
+    dev = device_index(codes, scales, w_codes, w_scales, offsets, out)
     codes, scales, k = _mx4_operand(codes, scales, "rows", 2)
     w_codes, w_scales, wk = _mx4_operand(w_codes, w_scales, "weights", 3 if grouped else 2)
     if k != wk:
         raise ValueError(f"rows have K = {k}, weights K = {wk}")
     mats, n = (w_codes.shape[0] if grouped else 1), w_codes.shape[-2]
-    if grouped and (offsets.dtype != torch.int32 or offsets.shape != (mats + 1,)):
-        raise ValueError(f"offsets must be int32 [{mats + 1}]")
+    at = None
+    if grouped:
+        if offsets.dtype is not torch.int32 or offsets.shape != (mats + 1,):
+            raise ValueError(f"offsets must be int32 [{mats + 1}]")
+        if not offsets.is_contiguous():
+            offsets = offsets.contiguous()
+        at = offsets.data_ptr()
     rows = codes.shape[0]
     if out is None:
-        out = torch.empty((rows, n), dtype=dtype, device=codes.device)
-    elif out.shape != (rows, n) or (n and out.stride(1) != 1) or (rows > 1 and out.stride(0) < n):
-        raise ValueError(f"out must be [{rows}, {n}] with dense rows")
-    dt = row_dtype(out.dtype)
-    with torch.cuda.device(codes.device):
-        M.moe_linear_mx4(codes.data_ptr(), scales.data_ptr(), rows, w_codes.data_ptr(), w_scales.data_ptr(),
-                         mats, offsets.contiguous().data_ptr() if grouped else None, n, k, out.data_ptr(), dt,
-                         max(out.stride(0), n), stream_of(codes))
+        out, ld = torch.empty((rows, n), dtype=dtype, device=codes.device), n
+    else:
+        ld = out.stride(0) if out.dim() == 2 and rows > 1 else n
+        if out.shape != (rows, n) or (n and out.stride(1) != 1) or ld < n:
+            raise ValueError(f"out must be [{rows}, {n}] with dense rows")
+    on_device(dev, M.moe_linear_mx4, codes.data_ptr(), scales.data_ptr(), rows, w_codes.data_ptr(),
+              w_scales.data_ptr(), mats, at, n, k, out.data_ptr(), row_dtype(out.dtype), ld)
     return out

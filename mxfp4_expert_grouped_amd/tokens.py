@@ -17,22 +17,23 @@ forward pass with it on ``x.detach().requires_grad_()``, or call
 
 from __future__ import annotations
 
-from dataclasses import dataclass
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import mxmoe as M
-from .layer import check_device, row_dtype, stream_of
+from .layer import device_index, on_device, row_dtype
 
 
-@dataclass(frozen=True)
 class TokenOrder:
     """Which row belongs to which (token, choice): see moe_sort_tokens."""
-    offsets: torch.Tensor    # int32 [E+1] first row of each expert; offsets[E] rows in all
-    row_src: torch.Tensor    # int32 [T*k] pair t*k + j of each row, -1 behind the last
-    token_row: torch.Tensor  # int32 [T, k] row of each pair, -1 for a dropped one
+    __slots__ = ("offsets", "row_src", "token_row")
+
+    def __init__(self, offsets: torch.Tensor, row_src: torch.Tensor, token_row: torch.Tensor):
+        self.offsets = offsets      # int32 [E+1] first row of each expert; offsets[E] rows in all
+        self.row_src = row_src      # int32 [T*k] pair t*k + j of each row, -1 behind the last
+        self.token_row = token_row  # int32 [T, k] row of each pair, -1 for a dropped one
 
     @property
     def num_experts(self) -> int:
@@ -60,58 +61,64 @@ def sort_tokens(ids: torch.Tensor, num_experts: int) -> TokenOrder:
     ids outside [0, num_experts) are dropped (-1: padding)."""
     if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"ids must be int32 or int64 [T, k], got {ids.dtype} with {ids.dim()} dimensions")
-    check_device(ids)
-    ids = ids.contiguous()
+    dev = device_index(ids)
+    if not ids.is_contiguous():
+        ids = ids.contiguous()
     t, k = ids.shape
     need = M.moe_sort_tokens_workspace_bytes(t, k, num_experts)
-    i32 = dict(dtype=torch.int32, device=ids.device)
-    offsets, row_src, token_row = torch.empty(num_experts + 1, **i32), torch.empty(t * k, **i32), torch.empty((t, k), **i32)
-    ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-    with torch.cuda.device(ids.device):
-        M.moe_sort_tokens(ids.data_ptr(), M.MOE_ID_INT64 if ids.dtype == torch.int64 else M.MOE_ID_INT32, t, k,
-                          num_experts, offsets.data_ptr(), row_src.data_ptr(), token_row.data_ptr(),
-                          ws.data_ptr() if need else None, need, stream_of(ids))
+    device = ids.device
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=device)
+    row_src = torch.empty(t * k, dtype=torch.int32, device=device)
+    token_row = torch.empty((t, k), dtype=torch.int32, device=device)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    on_device(dev, M.moe_sort_tokens, ids.data_ptr(),
+              M.MOE_ID_INT64 if ids.dtype is torch.int64 else M.MOE_ID_INT32, t, k, num_experts, offsets.data_ptr(),
+              row_src.data_ptr(), token_row.data_ptr(), ws.data_ptr() if need else None, need)
     return TokenOrder(offsets, row_src, token_row)
 
 
-def _matrix(x: torch.Tensor, rows: int, what: str) -> torch.Tensor:
-    """x [rows, d] with dense rows that do not overlap (else a copy)."""
+def _matrix(x: torch.Tensor, rows: int, what: str):
+    """x [rows, d] with dense rows that do not overlap (else a copy), and its row stride"""
     if x.dim() != 2 or x.shape[0] != rows:
         raise ValueError(f"{what} must be [{rows}, d], got {tuple(x.shape)}")
     d = x.shape[1]
-    return x if (d == 0 or x.stride(1) == 1) and (rows < 2 or x.stride(0) >= d) else x.contiguous()
-
-
-def _ld(x: torch.Tensor) -> int:
-    return max(x.stride(0), x.shape[1])
+    ld, step = x.stride()
+    if d == 0 or rows == 0:
+        return x, d
+    if step == 1 and (ld >= d or rows == 1):
+        return x, max(ld, d)
+    return x.contiguous(), d
 
 
 def _dispatch(x: torch.Tensor, order: TokenOrder) -> torch.Tensor:
-    x = _matrix(x, order.num_tokens, "x")
-    xs = torch.empty((order.capacity, x.shape[1]), dtype=x.dtype, device=x.device)
+    dev = device_index(x, order.token_row)
+    tr = order.token_row
+    t, k = tr.shape
+    x, ld = _matrix(x, t, "x")
+    d = x.shape[1]
+    xs = torch.empty((t * k, d), dtype=x.dtype, device=x.device)
     sz = x.element_size()
-    with torch.cuda.device(x.device):
-        M.moe_dispatch_rows(x.data_ptr(), x.shape[1] * sz, _ld(x) * sz, order.token_row.data_ptr(), order.num_tokens,
-                            order.top_k, order._num_rows(), order.capacity, xs.data_ptr(), xs.shape[1] * sz,
-                            stream_of(x))
+    on_device(dev, M.moe_dispatch_rows, x.data_ptr(), d * sz, ld * sz, tr.data_ptr(), t, k, order._num_rows(), t * k,
+              xs.data_ptr(), d * sz)
     return xs
 
 
 def _combine(rows: torch.Tensor, weights: Optional[torch.Tensor], order: TokenOrder) -> torch.Tensor:
-    rows = _matrix(rows, order.capacity, "rows")
+    dev = device_index(rows, weights, order.token_row)
+    tr = order.token_row
+    t, k = tr.shape
+    rows, ld = _matrix(rows, t * k, "rows")
+    if weights is not None and not weights.is_contiguous():
+        weights = weights.contiguous()
     d = rows.shape[1]
-    y = torch.empty((order.num_tokens, d), dtype=rows.dtype, device=rows.device)
-    with torch.cuda.device(rows.device):
-        M.moe_combine_rows(rows.data_ptr(), row_dtype(rows.dtype), order.capacity, d, _ld(rows),
-                           order.token_row.data_ptr(), weights.data_ptr() if weights is not None else None,
-                           order.num_tokens, order.top_k, y.data_ptr(), d, stream_of(rows))
+    y = torch.empty((t, d), dtype=rows.dtype, device=rows.device)
+    on_device(dev, M.moe_combine_rows, rows.data_ptr(), row_dtype(rows.dtype), t * k, d, ld, tr.data_ptr(),
+              weights.data_ptr() if weights is not None else None, t, k, y.data_ptr(), d)
     return y
 
 
 def dispatch_backward(dxs: torch.Tensor, order: TokenOrder) -> torch.Tensor:
     """Gradient of :func:`dispatch`: dx [T, d] from dxs [T*k, d]."""
-    row_dtype(dxs.dtype)
-    check_device(dxs, order.token_row)
     return _combine(dxs, None, order)
 
 
@@ -119,28 +126,31 @@ def combine_backward(dy: torch.Tensor, rows: Optional[torch.Tensor], weights: Op
                      order: TokenOrder, need_rows: bool = True, need_weights: bool = True):
     """Gradients of :func:`combine` from dy [T, d]: (drows [T*k, d] or None, dweights [T, k] or None).
     ``rows`` is needed for dweights only."""
-    dy = _matrix(dy, order.num_tokens, "dy")
-    dt, d = row_dtype(dy.dtype), dy.shape[1]
+    t, k = order.token_row.shape
+    dt = row_dtype(dy.dtype)
     if need_weights:
-        if rows is None or rows.dtype != dy.dtype or rows.dim() != 2 or rows.shape[1] != d:
+        if rows is None or rows.dtype != dy.dtype or rows.dim() != 2 or rows.shape[1] != dy.shape[-1]:
             raise ValueError("the gradient of the weights needs rows of dy's type and width")
-        rows = _matrix(rows, order.capacity, "rows")
+    else:
+        rows = None
     _check_weights(weights, order)
-    check_device(dy, rows if need_weights else None, weights, order.token_row)
-    weights = weights.contiguous() if weights is not None else None
-    drows = torch.empty((order.capacity, d), dtype=dy.dtype, device=dy.device) if need_rows else None
-    dw = torch.empty(order.token_row.shape, dtype=torch.float32, device=dy.device) if need_weights else None
-    with torch.cuda.device(dy.device):
-        M.moe_combine_rows_backward(
-            dy.data_ptr(), rows.data_ptr() if need_weights else None, dt, order.capacity, d, _ld(dy),
-            _ld(rows) if need_weights else d, order.token_row.data_ptr(),
-            weights.data_ptr() if weights is not None else None, order.num_tokens, order.top_k, order._num_rows(),
-            drows.data_ptr() if need_rows else None, d, dw.data_ptr() if need_weights else None, stream_of(dy))
+    dev = device_index(dy, rows, weights, order.token_row)
+    dy, ld_dy = _matrix(dy, t, "dy")
+    d = ld_rows = dy.shape[1]
+    if rows is not None:
+        rows, ld_rows = _matrix(rows, t * k, "rows")
+    if weights is not None:
+        weights = weights.contiguous()
+    drows = torch.empty((t * k, d), dtype=dy.dtype, device=dy.device) if need_rows else None
+    dw = torch.empty((t, k), dtype=torch.float32, device=dy.device) if need_weights else None
+    ptr = lambda x: x.data_ptr() if x is not None else None  # noqa: E731
+    on_device(dev, M.moe_combine_rows_backward, dy.data_ptr(), ptr(rows), dt, t * k, d, ld_dy, ld_rows,
+              order.token_row.data_ptr(), ptr(weights), t, k, order._num_rows(), ptr(drows), d, ptr(dw))
     return drows, dw
 
 
 def _check_weights(weights: Optional[torch.Tensor], order: TokenOrder) -> None:
-    if weights is not None and (weights.dtype != torch.float32 or weights.shape != order.token_row.shape):
+    if weights is not None and (weights.dtype is not torch.float32 or weights.shape != order.token_row.shape):
         raise ValueError(f"weights must be float32 {list(order.token_row.shape)}, got {weights.dtype} {list(weights.shape)}")
 
 
@@ -162,7 +172,7 @@ class _Combine(torch.autograd.Function):
         need_w = weights is not None and weights.requires_grad
         ctx.order = order
         ctx.save_for_backward(rows if need_w else None, weights)
-        return _combine(rows, weights.contiguous() if weights is not None else None, order)
+        return _combine(rows, weights, order)
 
     @staticmethod
     @once_differentiable
@@ -176,9 +186,9 @@ def dispatch(x: torch.Tensor, order: TokenOrder) -> torch.Tensor:
     """xs [T*k, d]: row r is the row of x of the token that ``order.row_src[r]`` belongs to; zeros behind
     the last row.  Any element type moves (MXFP4 codes and scales too); bf16, fp16 and fp32 have a gradient,
     dx[t] = sum of its rows' gradients in fp32."""
-    check_device(x, order.token_row)
-    if x.requires_grad:
-        row_dtype(x.dtype)
+    if not (x.requires_grad and torch.is_grad_enabled()):
+        return _dispatch(x, order)
+    row_dtype(x.dtype)
     return _Dispatch.apply(x, order)
 
 
@@ -187,5 +197,6 @@ def combine(rows: torch.Tensor, weights: Optional[torch.Tensor], order: TokenOrd
     (None: ones), in fp32, rounded once; a token whose pairs are all dropped gets zeros."""
     row_dtype(rows.dtype)
     _check_weights(weights, order)
-    check_device(rows, weights, order.token_row)
+    if not (torch.is_grad_enabled() and (rows.requires_grad or (weights is not None and weights.requires_grad))):
+        return _combine(rows, weights, order)
     return _Combine.apply(rows, weights, order)
