@@ -579,14 +579,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     constexpr int SZ = sizeof(T), PER = 16 / SZ;
     const uint64_t base = reinterpret_cast<uint64_t>(static_cast<T*>(a.y) + int64_t(t.row0) * a.ld_y + t.col0);
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, kNowhere, 0x00027000);
-    const int row = wm * MI * 32 + l32, cols = a.n - t.col0;
+    const int cols = a.n - t.col0;
     const uint32_t ld = static_cast<uint32_t>(a.ld_y) * SZ;
     // the last MFMA's results take 16 passes (18 wait states); the compiler
     // counts them for its own reads, not for the assembly's below
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-    uint32_t at[MI];
+    // this lane's rows: with 16-bit results lane l stores rows l%16 and
+    // 16 + l%16 of each block of 32, otherwise row l%32
+    constexpr bool HALVES = WIDE && SZ == 2;
+    constexpr int NR = HALVES ? 2 : 1;
+    uint32_t at[MI][NR];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) at[i] = row + 32 * i < t.rows ? (row + 32 * i) * ld : kNowhere;
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int h = 0; h < NR; ++h) {
+        const int row = (wm * MI + i) * 32 + (HALVES ? 16 * h + (lane & 15) : l32);
+        at[i][h] = row < t.rows ? row * ld : kNowhere;
+      }
     unrolled<0, NM>([&](auto bc) {
       constexpr int i = decltype(bc)::value / NI, j = decltype(bc)::value % NI;
       typedef uint32_t v4u __attribute__((ext_vector_type(4)));
@@ -600,31 +609,51 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
         asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(f) : "a"(r[x]));
         return f;
       };
-      auto put = [&](int cx, v4u v) {
-        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, cx < cols ? at[i] + cx * SZ : kNowhere, 0, 0);
+      auto put = [&](int h, int cx, v4u v) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, cx < cols ? at[i][h] + cx * SZ : kNowhere, 0, 0);
       };
+      const int col = (wn * NI + j) * 32;
+      if constexpr (HALVES) {
+        // lane (l32, g32) has columns 8q + 4 g32 .. + 3 of row l32, q = 0..3.
+        // Lanes l and l + 32 exchange halves, and it has 8 columns (16 bytes),
+        // 16p + 8 g32 .., p = 0, 1; then the 16-lane rows of the wave do, and
+        // four lanes have the 64 bytes of a row of the block.
+        uint32_t v[2][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = (wn * NI + j) * 32 + 8 * q;
-        if constexpr (!WIDE) {
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int cx = col + 4 * g32 + x;
-            const uint32_t off = cx < cols ? at[i] + cx * SZ : kNowhere;
-            const T v = from_f32<T>(c(4 * q + x));
-            if constexpr (SZ == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), rsrc, off, 0, 0);
-            else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, off, 0, 0);
+          for (int x = 0; x < 2; ++x) {
+            const auto e = __builtin_amdgcn_permlane32_swap(pack2<T>(c(8 * p + 2 * x), c(8 * p + 2 * x + 1)),
+                                                            pack2<T>(c(8 * p + 4 + 2 * x), c(8 * p + 5 + 2 * x)), false, false);
+            v[p][x] = e[0];
+            v[p][2 + x] = e[1];
           }
-        } else if constexpr (SZ == 4) {
-          const v4f v = {c(4 * q), c(4 * q + 1), c(4 * q + 2), c(4 * q + 3)};
-          put(col + 4 * g32, __builtin_bit_cast(v4u, v));
-        } else if (q % 2 == 0) {
-          // lanes l and l + 32 exchange halves: 16 bytes of a row each
-          const uint32_t x0 = pack2<T>(c(4 * q), c(4 * q + 1)), x1 = pack2<T>(c(4 * q + 2), c(4 * q + 3));
-          const uint32_t y0 = pack2<T>(c(4 * q + 4), c(4 * q + 5)), y1 = pack2<T>(c(4 * q + 6), c(4 * q + 7));
-          const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-          put(col + 8 * g32, v4u{s0[0], s1[0], s0[1], s1[1]});
+        v4u o[2];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const auto e = __builtin_amdgcn_permlane16_swap(v[0][x], v[1][x], false, false);
+          o[0][x] = e[0];
+          o[1][x] = e[1];
+        }
+        const int cx = col + 16 * ((lane >> 4) & 1) + 8 * g32;
+        put(0, cx, o[0]);
+        put(1, cx, o[1]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (WIDE) {
+            const v4f v = {c(4 * q), c(4 * q + 1), c(4 * q + 2), c(4 * q + 3)};
+            put(0, col + 8 * q + 4 * g32, __builtin_bit_cast(v4u, v));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int cx = col + 8 * q + 4 * g32 + x;
+              const uint32_t off = cx < cols ? at[i][0] + cx * SZ : kNowhere;
+              const T v = from_f32<T>(c(4 * q + x));
+              if constexpr (SZ == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), rsrc, off, 0, 0);
+              else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, off, 0, 0);
+            }
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
