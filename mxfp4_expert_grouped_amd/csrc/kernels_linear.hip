@@ -55,7 +55,12 @@ __device__ __forceinline__ void mat_rows(const LinearArgs& a, int e, int& lo, in
 // whole workgroup (part: a word of LDS per wave).  Returns the number of tiles.
 template <int THREADS, int TM>
 __device__ __forceinline__ int tile_prefix(const LinearArgs& a, int* prefix, int* part) {
-  constexpr int PER = kMaxMats / THREADS;
+  if (!a.offsets) {
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
+    return static_cast<int>((a.rows + TM - 1) / TM);
+  }
+  constexpr int PER = (kMaxMats + THREADS - 1) / THREADS;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int n[PER], sum = 0;
 #pragma unroll
@@ -120,87 +125,131 @@ __device__ __forceinline__ void store_cols(T* y, int64_t ld, int row, int col, i
 }
 
 // ---------------------------------------------------------------------------
-// A few rows per matrix: weight streaming.  A unit is 16 rows x 16 columns; a
-// persistent grid takes them round-robin, the columns of a tile fastest, so
-// that neighbouring workgroups stream neighbouring weight rows.  The four
-// waves of a workgroup share a unit's K: wave w takes the 512-wide groups w,
-// w + 4, ... (256 bytes of each of 16 weight rows, straight from memory to
-// registers in operand order), and the four partial sums meet in LDS in wave
-// order.  Bound by the weights' bytes.
+// Few products: straight from memory to registers in operand order.  A unit is
+// 16 MT rows x 16 NB columns; a persistent grid takes them round-robin, the
+// columns of a row tile fastest, so that neighbouring workgroups read
+// neighbouring weight rows.  The NW waves of a workgroup share a unit's K:
+// wave w takes the 512-wide groups w, w + NW, ... (256 bytes of each row), and
+// the partial sums meet in LDS in wave order.  With at most one unit per CU
+// NW is 8 and a wave has the next group's loads on their way while it
+// multiplies this one: the time is that of one or two loads.  With more units
+// NW is 4 and several workgroups per CU hide each other's loads.
 //
 // SCALES: how the scale bytes come.  0: 16 bytes for a row's four steps
 // (k % 512 == 0); 1: a dword per step (k % 128 == 0); 2: single bytes, with
 // the last step's missing blocks left out (any multiple of 32).
 // ---------------------------------------------------------------------------
-constexpr int kStreamThreads = 256, kStreamWaves = kStreamThreads / 64;
-
-template <typename T, int SCALES>
-__global__ void __launch_bounds__(kStreamThreads, 4) k_linear_stream(LinearArgs a, bool wide) {
+template <typename T, int SCALES, int MT, int NB, int NW>
+__global__ void __launch_bounds__(64 * NW, NW == 4 ? 4 : 2) k_linear_stream(LinearArgs a, bool wide) {
+  static_assert(MT * NB <= NW, "a wave joins one block of a unit");
   __shared__ int prefix[kMaxMats];
-  __shared__ int part[kStreamWaves];
-  __shared__ float4 sums[kStreamWaves][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ int part[NW];
+  __shared__ float4 sums[NW][MT * NB][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int r16 = lane & 15, g = lane >> 4;
-  const int tiles = tile_prefix<kStreamThreads, 16>(a, prefix, part);
-  const int cblocks = (a.n + 15) / 16;
+  const int tiles = tile_prefix<64 * NW, 16 * MT>(a, prefix, part);
+  const int cblocks = (a.n + 16 * NB - 1) / (16 * NB);
   const int64_t units = int64_t(tiles) * cblocks;
   const int nb = a.k / 32;                     // blocks of 32 along k
   const int groups = (nb + 15) / 16;
+  struct Operand {
+    uint4 v[4];
+    uint32_t s[4];
+  };
+  // group q of one row (its codes at c, its scales at s; ok: the row is there)
+  auto load = [&](Operand& o, const uint8_t* c, const uint8_t* s, bool ok, int q) {
+    if constexpr (SCALES == 0) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (ok) x = *reinterpret_cast<const uint4*>(s + 16 * q);
+      o.s[0] = x.x; o.s[1] = x.y; o.s[2] = x.z; o.s[3] = x.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = 16 * q + 4 * i + g;        // this lane's block
+      const bool in = ok && b < nb;
+      o.v[i] = make_uint4(0, 0, 0, 0);
+      if (in) o.v[i] = *reinterpret_cast<const uint4*>(c + 16 * int64_t(b));
+      if constexpr (SCALES == 1) o.s[i] = in ? *reinterpret_cast<const uint32_t*>(s + b - g) : 0;
+      if constexpr (SCALES == 2) o.s[i] = in ? s[b] : 0;
+    }
+  };
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int t = static_cast<int>(u / cblocks), cb = static_cast<int>(u - int64_t(t) * cblocks);
+    // (a 64-bit division takes a tenth of a short call)
+    const int t = static_cast<int>(units < (int64_t(1) << 31) ? static_cast<uint32_t>(u) / static_cast<uint32_t>(cblocks) : u / cblocks), cb = static_cast<int>(u - int64_t(t) * cblocks);
     const int e = tile_matrix(prefix, a.mats, t);
     int lo, hi;
     mat_rows(a, e, lo, hi);
-    lo += (t - prefix[e]) * 16;
-    const int row = lo + r16, col = cb * 16 + r16;
-    const bool row_ok = row < hi, col_ok = col < a.n;
-    const uint8_t* ap = a.a_c + int64_t(row) * (a.k / 2);
-    const uint8_t* as = a.a_s + int64_t(row) * nb;
-    const int64_t wrow = int64_t(e) * a.n + col;
-    const uint8_t* wp = a.w_c + wrow * (a.k / 2);
-    const uint8_t* ws = a.w_s + wrow * nb;
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int q = wave; q < groups; q += kStreamWaves) {
-      uint4 wv[4], av[4];
-      uint32_t wsc[4], asc[4];
-      if constexpr (SCALES == 0) {
-        uint4 x = make_uint4(0, 0, 0, 0), z = x;
-        if (col_ok) x = *reinterpret_cast<const uint4*>(ws + 16 * q);
-        if (row_ok) z = *reinterpret_cast<const uint4*>(as + 16 * q);
-        wsc[0] = x.x; wsc[1] = x.y; wsc[2] = x.z; wsc[3] = x.w;
-        asc[0] = z.x; asc[1] = z.y; asc[2] = z.z; asc[3] = z.w;
-      }
+    lo += (t - prefix[e]) * 16 * MT;
+    const uint8_t *ap[MT], *as[MT], *wp[NB], *ws[NB];
+    bool row_ok[MT], col_ok[NB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int kb = 16 * q + 4 * i + g;     // this lane's block
-        const bool in = kb < nb;
-        wv[i] = av[i] = make_uint4(0, 0, 0, 0);
-        if (in && col_ok) wv[i] = *reinterpret_cast<const uint4*>(wp + 16 * int64_t(kb));
-        if (in && row_ok) av[i] = *reinterpret_cast<const uint4*>(ap + 16 * int64_t(kb));
-        if constexpr (SCALES == 1) {
-          wsc[i] = in && col_ok ? *reinterpret_cast<const uint32_t*>(ws + kb - g) : 0;
-          asc[i] = in && row_ok ? *reinterpret_cast<const uint32_t*>(as + kb - g) : 0;
-        } else if constexpr (SCALES == 2) {
-          wsc[i] = in && col_ok ? ws[kb] : 0;
-          asc[i] = in && row_ok ? as[kb] : 0;
-        }
-      }
+    for (int i = 0; i < MT; ++i) {
+      const int row = lo + 16 * i + r16;
+      row_ok[i] = row < hi;
+      ap[i] = a.a_c + int64_t(row) * (a.k / 2);
+      as[i] = a.a_s + int64_t(row) * nb;
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int sh = SCALES == 2 ? 0 : 8 * g;
-        acc = mfma_fp4(wv[i], av[i], acc, wsc[i] >> sh, asc[i] >> sh);
+    for (int j = 0; j < NB; ++j) {
+      const int col = (cb * NB + j) * 16 + r16;
+      col_ok[j] = col < a.n;
+      wp[j] = a.w_c + (int64_t(e) * a.n + col) * (a.k / 2);
+      ws[j] = a.w_s + (int64_t(e) * a.n + col) * nb;
+    }
+    v4f acc[MT][NB];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    auto loads = [&](Operand* x, Operand* w, int q) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) load(w[j], wp[j], ws[j], col_ok[j], q);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) load(x[i], ap[i], as[i], row_ok[i], q);
+    };
+    auto products = [&](const Operand* x, const Operand* w) {
+      const int sh = SCALES == 2 ? 0 : 8 * g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[i][j] = mfma_fp4(w[j].v[k], x[i].v[k], acc[i][j], w[j].s[k] >> sh, x[i].s[k] >> sh);
+    };
+    if constexpr (MT * NB == 1 && NW == 8) {
+      Operand x[2], w[2];
+      int q = wave;
+      if (q < groups) loads(&x[0], &w[0], q);
+      while (q < groups) {
+        if (q + NW < groups) loads(&x[1], &w[1], q + NW);
+        products(&x[0], &w[0]);
+        x[0] = x[1];
+        w[0] = w[1];
+        q += NW;
+      }
+    } else {
+      Operand x[MT], w[NB];
+      for (int q = wave; q < groups; q += NW) {
+        loads(x, w, q);
+        products(x, w);
       }
     }
-    sums[wave][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    __syncthreads();
-    if (wave == 0) {
-      v4f s = acc;
 #pragma unroll
-      for (int w = 1; w < kStreamWaves; ++w) {
-        const float4 p = sums[w][lane];
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        sums[wave][i * NB + j][lane] = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+    __syncthreads();
+    // waves 0 .. MT NB - 1 each join one block of the unit
+    if (wave < MT * NB) {
+      v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float4 p = sums[w][wave][lane];
         s[0] += p.x; s[1] += p.y; s[2] += p.z; s[3] += p.w;
       }
-      if (lo + r16 < hi) store_cols(static_cast<T*>(a.y), a.ld_y, lo + r16, cb * 16 + 4 * g, a.n, wide, s);
+      const int row = lo + 16 * (wave / NB) + r16;
+      if (row < hi) store_cols(static_cast<T*>(a.y), a.ld_y, row, (cb * NB + wave % NB) * 16 + 4 * g, a.n, wide, s);
     }
     __syncthreads();
   }
@@ -230,12 +279,15 @@ __global__ void __launch_bounds__(kStreamThreads, 4) k_linear_stream(LinearArgs 
 // wide, cost a quarter of the copies' rate: 95 against 75 us for the copies
 // alone of 8192 x 4096 x 7168.
 //
-// Scales.  AG (k % 512 == 0, scale rows on 16 bytes): one 16-byte piece per
-// row holds two steps' scales, copied every second step into one of two
-// buffers and kept in registers for those steps.  Otherwise two dwords per row
-// and step, in the slot.  A dword holds half a step's scales, byte 2q + g32
-// that of its quarter q of lane (l32, g32): shifted by 8 g32 once per step,
-// the MFMA takes byte 2q.
+// Scales come in pieces of GS steps, 8 GS bytes of each row, into one of two
+// buffers, from where every second step 16 bytes per row go to registers: GS
+// = 4 (k % 1024 == 0; 64-row tiles, whose rows are many for their products)
+// or 2 (k % 512 == 0), scale rows on 16 bytes; GS = 0 otherwise: two dwords
+// per row and step, in the slot.  The number of pieces matters more than their
+// bytes: 4096 rows over 64 matrices of 4096 x 7168 take 213 us without any,
+// 243 us with GS = 2.  A dword holds half a step's scales, byte 2q + g32 that
+// of its quarter q of lane (l32, g32): shifted by 8 g32 once per step, the
+// MFMA takes byte 2q.
 //
 // With k % 256 == 128 a row's last step is half a step: its copies bring the
 // first 64 bytes twice, and it has two quarters.  Rows past the tile's or the
@@ -250,6 +302,11 @@ typedef __attribute__((address_space(3))) void lds_void;
 // counts its own copies.  M0 holds the LDS address.
 __device__ __forceinline__ void copy16(uint32_t off, const uint8_t* base, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+// the same with the non-temporal hint
+__device__ __forceinline__ void copy16_nt(uint32_t off, const uint8_t* base, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "s"(lds)
                : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(uint32_t off, const uint8_t* base, uint32_t lds) {
@@ -307,18 +364,23 @@ constexpr int kTileN = 256, kTileThreads = 256;
 constexpr int kMaxTiles = 1 << 30;
 constexpr int kPanel = 4;  // row tiles that share a column block's weights in time
 
-template <int SZ, int BM, bool AG>
+template <int SZ, int BM, int GS>
 struct TileShape {
   static constexpr int WM = BM == 64 ? 1 : 2, WN = 4 / WM;        // waves along rows, columns
   static constexpr int MI = BM / WM / 32, NI = kTileN / WN / 32;  // 32-row, 32-column blocks of a wave
   static constexpr int S = BM == 256 ? 2 : 3;                     // ring slots
   static constexpr int A = 0, W = BM * 128, SC = W + kTileN * 128;  // slot: activations, weights, scale dwords
-  static constexpr int SLOT = SC + (AG ? 0 : (BM + kTileN) * 8);
-  static constexpr int GROUP = S * SLOT;                          // scale pieces of AG, two buffers
-  static constexpr int LDS = GROUP + (AG ? 2 * (BM + kTileN) * 16 : 0);
+  static constexpr int SLOT = SC + (GS ? 0 : (BM + kTileN) * 8);
+  static constexpr int GROUP = S * SLOT, PIECE = 8 * GS;          // scale pieces, two buffers
+  static constexpr int LDS = GROUP + 2 * (BM + kTileN) * PIECE;
+  static constexpr int U = GS ? GS : 1;                           // steps that are unrolled
   static constexpr int CA = BM / 32, CW = 8;                      // copies of codes per wave and step
-  // copies of a wave for a step, the first (i even) or second of its pair
-  static constexpr int copies(int i) { return CA + CW + (AG ? (i % 2 == 0 ? 2 : 0) : 4); }
+  // of scales: rows per copy, copies of a wave (waves that have none left
+  // over repeat another's, so that all count alike)
+  static constexpr int PR = GS ? 1024 / PIECE : 64;
+  static constexpr int CSA = GS ? (BM / PR + 3) / 4 : 2, CSW = GS ? kTileN / PR / 4 : 2;
+  // copies of a wave for a step, the i-th of its group
+  static constexpr int copies(int i) { return CA + CW + (i % U == 0 ? CSA + CSW : 0); }
   static constexpr int copies_from(int i, int n) { return n <= 0 ? 0 : copies(i) + copies_from(i + 1, n - 1); }
   // those issued in the last quarter before their step's slot is S - 1 steps
   // away: half of them with two slots (they have to land soon), else a quarter
@@ -327,10 +389,13 @@ struct TileShape {
 };
 
 // WIDE: n and the rows of y are whole numbers of 16-byte pieces.
-template <typename T, int BM, bool AG, bool WIDE>
+// ONCE: nearly every matrix has one row tile, so its weights are read once:
+// their copies carry the non-temporal hint (16 rows for 16 of 64 matrices of
+// 4096 x 7168: 43.7 against 46.7 us; with several row tiles it costs 5 %).
+template <typename T, int BM, int GS, bool WIDE, bool ONCE>
 __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
-  using P = TileShape<sizeof(T), BM, AG>;
-  constexpr int S = P::S, MI = P::MI, NI = P::NI, NM = MI * NI;
+  using P = TileShape<sizeof(T), BM, GS>;
+  constexpr int S = P::S, U = P::U, MI = P::MI, NI = P::NI, NM = MI * NI;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[P::LDS];
   __shared__ int prefix[kMaxMats];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
@@ -343,7 +408,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   // limit; only ranges that overlap could have more)
   const int total = min(mtiles, kMaxTiles / ntn) * ntn;
   const int nsteps = (a.k + 255) / 256;
-  const bool odd = !AG && (a.k & 128);  // the last step is half a step
+  const bool odd = !GS && (a.k & 128);  // the last step is half a step
 
   // ---- which tiles are this workgroup's: runs of gridDim/8 consecutive
   // tiles go to one XCD (workgroups go to the XCDs round-robin), so that the
@@ -385,9 +450,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)lds));
   int iss_pos = first, iss_step = 0, iss_slot = 0, iss_group = 0;
   const uint8_t *ia = nullptr, *iw = nullptr, *ias = nullptr, *iws = nullptr;  // the tile's first row, column
-  uint32_t oa[P::CA], ow[P::CW], osa, osw;
+  uint32_t oa[P::CA], ow[P::CW], osa[GS ? P::CSA : 1], osw[GS ? P::CSW : 1];
   const int kb = a.k / 2, sb = a.k / 32;
-  const int sa_blk = wave % (BM / 64);  // 64-row block of activation scales that this wave copies
+  // block of PR activation rows whose scales this wave's copy number n brings
+  auto sa_blk = [&](int n) { return (P::CSA * wave + n) % (BM / P::PR); };
   // half a step's copies: chunks 4-7 are not there, the first four come again
   const int chunk = (lane & 7) ^ (lane >> 3);
   const uint32_t half_back = chunk & 4 ? 64 : 0;
@@ -402,8 +468,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     for (int q = 0; q < P::CA; ++q) oa[q] = min(8 * (P::CA * wave + q) + (lane >> 3), rlast) * kb + 16 * chunk;
 #pragma unroll
     for (int q = 0; q < P::CW; ++q) ow[q] = min(8 * (P::CW * wave + q) + (lane >> 3), clast) * kb + 16 * chunk;
-    osa = min(64 * sa_blk + lane, rlast) * sb;
-    osw = min(64 * wave + lane, clast) * sb;
+    constexpr int LR = 64 / P::PR;  // lanes that share a row's piece
+#pragma unroll
+    for (int n = 0; n < (GS ? P::CSA : 1); ++n)
+      osa[n] = min(P::PR * (GS ? sa_blk(n) : wave % (BM / 64)) + lane / LR, rlast) * sb + 16 * (lane % LR);
+#pragma unroll
+    for (int n = 0; n < (GS ? P::CSW : 1); ++n)
+      osw[n] = min(P::PR * (GS ? P::CSW * wave + n : wave) + lane / LR, clast) * sb + 16 * (lane % LR);
   };
   // (total and G are at most 2^30: no overflow)
   auto next_pos = [&](int pos) { return pos + G; };
@@ -414,16 +485,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     const bool half = odd && iss_step == nsteps - 1;
     const uint32_t back = half ? half_back : 0;
     if constexpr (m < P::CA) copy16(oa[m] - back, ia, slot + P::A + (P::CA * wave + m) * 1024);
+    else if constexpr (n < 0 && ONCE) copy16_nt(ow[m - P::CA] - back, iw, slot + P::W + (P::CW * wave + m - P::CA) * 1024);
     else if constexpr (n < 0) copy16(ow[m - P::CA] - back, iw, slot + P::W + (P::CW * wave + m - P::CA) * 1024);
-    else if constexpr (!AG) {
+    else if constexpr (!GS) {
       // dword n/2 of the step (half a step has one: it comes again)
-      const uint32_t d = n >= 2 && !half ? 4 : 0;
-      if constexpr (n % 2 == 0) copy4(osa + d, ias, slot + P::SC + (n / 2) * (BM + kTileN) * 4 + sa_blk * 256);
-      else copy4(osw + d, iws, slot + P::SC + (n / 2) * (BM + kTileN) * 4 + BM * 4 + wave * 256);
+      const uint32_t d = n >= 2 && !half ? 4 : 0, at = slot + P::SC + (n / 2) * (BM + kTileN) * 4;
+      if constexpr (n % 2 == 0) copy4(osa[0] + d, ias, at + wave % (BM / 64) * 256);
+      else copy4(osw[0] + d, iws, at + BM * 4 + wave * 256);
     } else if constexpr (I == 0) {
-      const uint32_t buf = lds0 + P::GROUP + iss_group * (BM + kTileN) * 16;
-      if constexpr (n == 0) copy16(osa, ias, buf + sa_blk * 1024);
-      else copy16(osw, iws, buf + BM * 16 + wave * 1024);
+      const uint32_t buf = lds0 + P::GROUP + iss_group * (BM + kTileN) * P::PIECE;
+      if constexpr (n < P::CSA) copy16(osa[n], ias, buf + sa_blk(n) * 1024);
+      else copy16(osw[n - P::CSA], iws, buf + BM * P::PIECE + (P::CSW * wave + n - P::CSA) * 1024);
     }
   };
   // to the next step; behind the last tile the last one is copied again, into
@@ -433,17 +505,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     iss_slot = iss_slot + 1 == S ? 0 : iss_slot + 1;
     ia += 128;
     iw += 128;
-    if (!AG) {
-      ias += 8;
-      iws += 8;
-    } else if (I == 1) {
-      ias += 16;
-      iws += 16;
+    if (I == U - 1) {
+      ias += 8 * U;
+      iws += 8 * U;
       iss_group ^= 1;
     }
     ++iss_step;
-    // (with AG a tile ends with a pair of steps)
-    if ((!AG || I == 1) && iss_step == nsteps) {
+    // (a tile ends with a group of steps)
+    if (I == U - 1 && iss_step == nsteps) {
       iss_step = 0;
       if (next_pos(iss_pos) < total) iss_pos = next_pos(iss_pos);
       iss_setup(tile_at(iss_pos));
@@ -456,7 +525,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   const int ch[4] = {16 * (g32 ^ (l32 & 7)), 16 * ((2 + g32) ^ (l32 & 7)), 16 * ((4 + g32) ^ (l32 & 7)),
                      16 * ((6 + g32) ^ (l32 & 7))};
   uint4 av[2][MI], wv[2][NI];       // the fragments of this quarter and of the next
-  uint4 agr[MI], wgr[NI];           // AG: two steps' scales
+  uint4 agr[MI], wgr[NI];           // GS: two steps' scales
   uint2 araw[MI], wraw[NI];         // otherwise the next step's
   uint32_t asc[2][MI], wsc[2][NI];  // this step's, of its first and second half
   auto read_frag = [&](int slot, auto hc, auto jc) {
@@ -465,16 +534,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     if constexpr (j < NI) wv[H % 2][j] = *reinterpret_cast<const uint4*>(p + fw + ch[H] + j * 4096);
     else av[H % 2][j - NI] = *reinterpret_cast<const uint4*>(p + fa + ch[H] + (j - NI) * 4096);
   };
-  // scales of the step in `slot`, the I-th of its pair (scale buffer grp)
+  // scales of the step in `slot`, the I-th of its group (scale buffer grp)
   auto read_scales = [&](int slot, int grp, auto ic) {
     constexpr int I = decltype(ic)::value;
-    if constexpr (AG) {
-      if constexpr (I == 0) {
-        const uint8_t* p = lds + P::GROUP + grp * (BM + kTileN) * 16;
+    if constexpr (GS) {
+      if constexpr (I % 2 == 0) {
+        const uint8_t* p = lds + P::GROUP + grp * (BM + kTileN) * P::PIECE + 8 * I;
 #pragma unroll
-        for (int j = 0; j < NI; ++j) wgr[j] = *reinterpret_cast<const uint4*>(p + (BM + (wn * NI + j) * 32 + l32) * 16);
+        for (int j = 0; j < NI; ++j) wgr[j] = *reinterpret_cast<const uint4*>(p + (BM + (wn * NI + j) * 32 + l32) * P::PIECE);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) agr[i] = *reinterpret_cast<const uint4*>(p + ((wm * MI + i) * 32 + l32) * 16);
+        for (int i = 0; i < MI; ++i) agr[i] = *reinterpret_cast<const uint4*>(p + ((wm * MI + i) * 32 + l32) * P::PIECE);
       }
     } else {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(lds + slot * P::SLOT + P::SC);
@@ -495,13 +564,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     const int sh = 8 * g32;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      wsc[0][j] = (AG ? (I == 0 ? wgr[j].x : wgr[j].z) : wraw[j].x) >> sh;
-      wsc[1][j] = (AG ? (I == 0 ? wgr[j].y : wgr[j].w) : wraw[j].y) >> sh;
+      wsc[0][j] = (GS ? (I % 2 == 0 ? wgr[j].x : wgr[j].z) : wraw[j].x) >> sh;
+      wsc[1][j] = (GS ? (I % 2 == 0 ? wgr[j].y : wgr[j].w) : wraw[j].y) >> sh;
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      asc[0][i] = (AG ? (I == 0 ? agr[i].x : agr[i].z) : araw[i].x) >> sh;
-      asc[1][i] = (AG ? (I == 0 ? agr[i].y : agr[i].w) : araw[i].y) >> sh;
+      asc[0][i] = (GS ? (I % 2 == 0 ? agr[i].x : agr[i].z) : araw[i].x) >> sh;
+      asc[1][i] = (GS ? (I % 2 == 0 ? agr[i].y : agr[i].w) : araw[i].y) >> sh;
     }
   };
 
@@ -515,7 +584,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
       for (int j = 0; j < NI; ++j) asm volatile("" : "+a"(acc[i][j]));
   };
   int slot = 0, group = 0;
-  // One step, the I-th of its pair, of NQ quarters (4, or 2 for half a step).
+  // One step, the I-th of its group, of NQ quarters (4, or 2 for half a step).
   // FIRST: the tile's first, its products start from zero.  after_stores: the
   // last tile's stores may still be on their way (operations finish in the
   // order in which they were issued).
@@ -526,7 +595,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     shift_scales(ic);
     // the copies of step s + S - 1, begun in the last quarter of step s - 1,
     // go on over the quarters before the barrier (with two slots: the first)
-    constexpr int IP = (I + S - 1) % 2, CP = P::copies(IP), C0 = P::first_part(IP);
+    constexpr int IP = (I + S - 1) % U, CP = P::copies(IP), C0 = P::first_part(IP);
     constexpr int QI = S == 2 ? 1 : NQ - 1;  // quarters that issue them
     unrolled<0, NQ>([&](auto qc) {
       constexpr int q = decltype(qc)::value;
@@ -549,7 +618,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
       unrolled<0, NM>([&](auto kc) {
         constexpr int k = decltype(kc)::value, i = k / NI, j = k % NI;
         acc[i][j] = mfma32_fp4<q % 2>(wv[q % 2][j], av[q % 2][i], FIRST && q == 0 ? v16f{} : acc[i][j], wsc[q / 2][j], asc[q / 2][i]);
-        if constexpr (LAST && k == 0) read_scales(nslot, I == 1 ? group ^ 1 : group, Int<(I + 1) % 2>{});
+        if constexpr (LAST && k == 0) read_scales(nslot, I == U - 1 ? group ^ 1 : group, Int<(I + 1) % U>{});
         // the next quarter's reads, in the first three quarters of this one
         constexpr int R = MI + NI, lo = k * R / (NM * 3 / 4), hi = (k + 1) * R / (NM * 3 / 4);
         unrolled<(lo < R ? lo : R), (hi < R ? hi : R)>(
@@ -560,14 +629,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
         }
         if constexpr (LAST) {
           constexpr int C = P::first_part(I + S);
-          unrolled<k * C / NM, (k + 1) * C / NM>([&](auto mc) { issue(Int<(I + S) % 2>{}, mc); });
+          unrolled<k * C / NM, (k + 1) * C / NM>([&](auto mc) { issue(Int<(I + S) % U>{}, mc); });
         }
         __builtin_amdgcn_sched_barrier(0);
       });
     });
     settle();
     slot = nslot;
-    if (I == 1) group ^= 1;
+    if (I == U - 1) group ^= 1;
   };
 
   // ---- results: acc[i][j] of this wave.  Buffer stores with the tile's first
@@ -664,11 +733,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   // are on their way before the first product
   iss_setup(tile_at(iss_pos));
   unrolled<0, S - 1>([&](auto sc) {
-    constexpr int I = decltype(sc)::value % 2;
+    constexpr int I = decltype(sc)::value % U;
     unrolled<0, P::copies(I)>([&](auto mc) { issue(Int<I>{}, mc); });
     advance(Int<I>{});
   });
-  unrolled<0, P::first_part(S - 1)>([&](auto mc) { issue(Int<(S - 1) % 2>{}, mc); });
+  unrolled<0, P::first_part(S - 1)>([&](auto mc) { issue(Int<(S - 1) % U>{}, mc); });
   wait_vm<P::copies_from(1, S - 2) + P::first_part(S - 1)>();
   tile_barrier();
   read_scales(0, 0, Int<0>{});
@@ -680,12 +749,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     // a store that did not go by 16-byte pieces is not counted: wait for it
     if (!WIDE && stored) wait_vm<0>();
     stored &= WIDE;
-    if constexpr (AG) {
+    if constexpr (GS) {
       step(Int<0>{}, Int<4>{}, Int<1>{}, stored);
       step(Int<1>{}, Int<4>{}, Int<0>{}, false);
-      for (int s = 2; s < nsteps; s += 2) {
+      if constexpr (U == 4) {
+        step(Int<2>{}, Int<4>{}, Int<0>{}, false);
+        step(Int<3>{}, Int<4>{}, Int<0>{}, false);
+      }
+      for (int s = U; s < nsteps; s += U) {
         step(Int<0>{}, Int<4>{}, Int<0>{}, false);
         step(Int<1>{}, Int<4>{}, Int<0>{}, false);
+        if constexpr (U == 4) {
+          step(Int<2>{}, Int<4>{}, Int<0>{}, false);
+          step(Int<3>{}, Int<4>{}, Int<0>{}, false);
+        }
       }
     } else {
       // half a step, if there is one, comes last; alone it is the first too
@@ -705,21 +782,38 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   wait_vm<0>();
 }
 
-// four columns of a row can be stored at once
-bool wide_stores(const LinearArgs& a, int64_t sz) { return rows_aligned(a.y, a.ld_y * sz, 4 * sz); }
+// Row tiles of BM rows: known for one matrix, otherwise an estimate (the
+// offsets are on the device): half a tile more per matrix than full ones, and
+// at least one for every row or matrix.
+int64_t row_tiles(const LinearArgs& a, int64_t bm) {
+  if (!a.offsets) return (a.rows + bm - 1) / bm;
+  return std::max<int64_t>((a.rows + bm - 1) / bm + a.mats / 2, std::min<int64_t>(a.rows, a.mats));
+}
+// at most so many
+int64_t row_tiles_max(const LinearArgs& a, int64_t bm) {
+  return a.offsets ? std::min<int64_t>(a.rows, (a.rows + bm - 1) / bm + a.mats) : (a.rows + bm - 1) / bm;
+}
+
+template <typename T, int SCALES, int MT, int NB, int NW>
+hipError_t stream_v(const LinearArgs& a, hipStream_t st) {
+  const int64_t units = row_tiles_max(a, 16 * MT) * ((a.n + 16 * NB - 1) / (16 * NB));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, (NW == 4 ? 8 : 2) * a.num_cus));
+  // four columns of a row can be stored at once
+  const bool wide = rows_aligned(a.y, a.ld_y * sizeof(T), 4 * sizeof(T));
+  k_linear_stream<T, SCALES, MT, NB, NW><<<grid, 64 * NW, 0, st>>>(a, wide);
+  return hipGetLastError();
+}
 
 template <typename T>
 hipError_t stream_t(const LinearArgs& a, hipStream_t st) {
-  const int64_t tiles = a.offsets ? std::min<int64_t>(a.rows, (a.rows + 15) / 16 + a.mats) : (a.rows + 15) / 16;
-  const int64_t units = tiles * ((a.n + 15) / 16);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, 8 * a.num_cus));
-  const bool wide = wide_stores(a, sizeof(T));
   const int64_t sb = a.k / 32;
   auto on = [&](int64_t al) { return rows_aligned(a.a_s, sb, al) && rows_aligned(a.w_s, sb, al); };
-  if (a.k % 512 == 0 && on(16)) k_linear_stream<T, 0><<<grid, kStreamThreads, 0, st>>>(a, wide);
-  else if (a.k % 128 == 0 && on(4)) k_linear_stream<T, 1><<<grid, kStreamThreads, 0, st>>>(a, wide);
-  else k_linear_stream<T, 2><<<grid, kStreamThreads, 0, st>>>(a, wide);
-  return hipGetLastError();
+  const bool one = row_tiles_max(a, 16) * ((a.n + 15) / 16) <= a.num_cus;
+  if (a.k % 512 == 0 && on(16)) return one ? stream_v<T, 0, 1, 1, 8>(a, st) : stream_v<T, 0, 1, 1, 4>(a, st);
+  if (a.k % 128 == 0 && on(4)) return one ? stream_v<T, 1, 1, 1, 8>(a, st) : stream_v<T, 1, 1, 1, 4>(a, st);
+  // what the tile kernel does not take comes here at every size: many rows in
+  // units of 64 x 32, which read half as much per product
+  return a.rows > 32 * a.mats ? stream_v<T, 2, 4, 2, 8>(a, st) : stream_v<T, 2, 1, 1, 4>(a, st);
 }
 
 template <typename T, int BM>
@@ -729,30 +823,51 @@ hipError_t tile_t(const LinearArgs& a, hipStream_t st) {
   // (single-element stores and 256 rows need more registers than there are)
   if constexpr (BM == 256)
     if (!wide) return tile_t<T, 128>(a, st);
-  const int64_t mtiles = a.offsets ? std::min<int64_t>(a.rows, (a.rows + BM - 1) / BM + a.mats) : (a.rows + BM - 1) / BM;
-  const int64_t tiles = mtiles * ((a.n + kTileN - 1) / kTileN);
+  const bool pieces = a.k % 512 == 0 && rows_aligned(a.a_s, sb, 16) && rows_aligned(a.w_s, sb, 16);
+  const bool once = a.rows <= (a.offsets ? 32 * a.mats : 64);
+  const int64_t tiles = row_tiles_max(a, BM) * ((a.n + kTileN - 1) / kTileN);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, a.num_cus));
-  if (!wide) {
-    if constexpr (BM != 256) k_linear_tile<T, BM, false, false><<<grid, kTileThreads, 0, st>>>(a);
-  } else if (a.k % 512 == 0 && rows_aligned(a.a_s, sb, 16) && rows_aligned(a.w_s, sb, 16)) {
-    k_linear_tile<T, BM, true, true><<<grid, kTileThreads, 0, st>>>(a);
-  } else {
-    k_linear_tile<T, BM, false, true><<<grid, kTileThreads, 0, st>>>(a);
+  auto go = [&](auto k) {
+    k<<<grid, kTileThreads, 0, st>>>(a);
+    return hipGetLastError();
+  };
+  if constexpr (BM != 256)
+    if (!wide) return go(k_linear_tile<T, BM, 0, false, false>);
+  if constexpr (BM == 64) {
+    if (pieces && a.k % 1024 == 0)
+      return once ? go(k_linear_tile<T, BM, 4, true, true>) : go(k_linear_tile<T, BM, 4, true, false>);
+    if (once) return pieces ? go(k_linear_tile<T, BM, 2, true, true>) : go(k_linear_tile<T, BM, 0, true, true>);
   }
-  return hipGetLastError();
+  return pieces ? go(k_linear_tile<T, BM, 2, true, false>) : go(k_linear_tile<T, BM, 0, true, false>);
 }
 
+// Which kernel, by estimates of their times in units of 0.1 us.
+// Tiles: one round of tiles (one per CU) takes 2 us and, per step of 256 of K,
+// 0.6, 0.8 and 1.3 us for 64, 128 and 256 rows when few CUs are busy; a full
+// chip takes about twice that for each (measured with k = 7168: 256 rows x
+// 4096 columns in 64 tiles of 64 rows 23 us, in 16 of 256 rows 38 us; 131072
+// rows over 64 matrices in 256-row tiles 314 us, in 64-row tiles 465 us), so
+// the same weights rank them in both cases.
+// Stream: 2 us, and 0.25 us per 256 units and 512 of K (measured: 64 rows x
+// 4096 columns, k = 7168, 16.8 us against 19.6 us in tiles; 128 rows 30
+// against 22 us; 16 rows 10 against 18 us).
 template <typename T>
 hipError_t linear_t(const LinearArgs& a, hipStream_t st) {
-  // rows per matrix on average; the offsets are on the device
-  const int64_t avg = a.rows / a.mats;
   const int64_t sb = a.k / 32;
   // (the tile kernel's stores reach 2^31 bytes from a tile's first row)
-  if (a.ld_y * sizeof(T) * 256 > (int64_t(1) << 31)) return stream_t<T>(a, st);
-  if (a.k % 128 || !rows_aligned(a.a_s, sb, 4) || !rows_aligned(a.w_s, sb, 4) || avg <= 16) return stream_t<T>(a, st);
-  if (avg <= 96) return tile_t<T, 64>(a, st);
-  if (avg <= 192) return tile_t<T, 128>(a, st);
-  return tile_t<T, 256>(a, st);
+  if (a.k % 128 || !rows_aligned(a.a_s, sb, 4) || !rows_aligned(a.w_s, sb, 4) ||
+      a.ld_y * sizeof(T) * 256 > (int64_t(1) << 31))
+    return stream_t<T>(a, st);
+  const int64_t cblocks = (a.n + kTileN - 1) / kTileN, steps = (a.k + 255) / 256;
+  auto tile_cost = [&](int64_t bm, int64_t step) {
+    return (row_tiles(a, bm) * cblocks + a.num_cus - 1) / a.num_cus * (20 + steps * step);
+  };
+  const int64_t c64 = tile_cost(64, 6), c128 = tile_cost(128, 8), c256 = tile_cost(256, 13);
+  const int64_t units = row_tiles(a, 16) * ((a.n + 15) / 16);
+  const int64_t stream = 20 + units * ((a.k + 511) / 512) * 25 / 2560;
+  const int64_t least = std::min(c64, std::min(c128, c256));
+  if (stream < least) return stream_t<T>(a, st);
+  return least == c64 ? tile_t<T, 64>(a, st) : least == c128 ? tile_t<T, 128>(a, st) : tile_t<T, 256>(a, st);
 }
 
 }  // namespace

@@ -220,7 +220,37 @@ def test_linear_by_experts(L, k, counts, n, dtype):
     assert_linear(run_linear(L, ac, asc, wc, wsc, offsets, dtype), y, mag, k, dtype)
 
 
-@pytest.mark.parametrize("k,n,per", [(512, 64, 2), (512, 200, 40), (512, 300, 200), (96, 40, 20)])
+# enough products for tiles of 64, 128 and 256 rows, whole and ragged ones; widths that are whole 16-byte pieces
+# of y, or not; every way in which the scales come (k a multiple of 1024, 512, 256, 128) with few and several steps
+@pytest.mark.parametrize("k", [128, 256, 384, 512, 640, 1024, 1536, 2048])
+@pytest.mark.parametrize("rows,n,dtype", [(500, 8192, "bf16"), (300, 8184, "fp32"), (1001, 8192, "bf16"), (1024, 8190, "fp16"),
+                                          (2000, 8184, "bf16"), (2048, 8192, "fp32"), (2047, 8191, "bf16"), (33, 12000, "fp32")])
+def test_linear_in_tiles(L, k, rows, n, dtype):
+    ac, asc = random_mx4((rows,), k, 500 + k + rows)
+    wc, wsc = random_mx4((1, n), k, 600 + k + n)
+    if dtype == "fp16":
+        asc -= 6
+    y, mag = linear_ref(ac, asc, wc, wsc, [0, rows])
+    assert_linear(run_linear(L, ac, asc, wc, wsc, None, dtype, grouped=False), y, mag, k, dtype)
+
+
+@pytest.mark.parametrize("k", [128, 384, 512, 1024, 1536])
+@pytest.mark.parametrize("counts,n,dtype", [
+    ([0, 300, 17, 64, 65, 128, 129, 1, 255, 256, 257, 0, 90, 33, 500, 63], 2304, "bf16"),
+    ([1, 0, 2, 64, 1] * 13, 2048, "fp32"), ([40] * 40 + [0] * 20, 1544, "fp16"), ([700, 0, 0, 900], 4088, "fp32"),
+])
+def test_linear_by_experts_in_tiles(L, k, counts, n, dtype):
+    offsets = [0] + np.cumsum(counts).tolist()
+    ac, asc = random_mx4((offsets[-1],), k, 700 + k + n)
+    wc, wsc = random_mx4((len(counts), n), k, 800 + k + n)
+    if dtype == "fp16":
+        asc -= 6
+    y, mag = linear_ref(ac, asc, wc, wsc, offsets)
+    assert_linear(run_linear(L, ac, asc, wc, wsc, offsets, dtype), y, mag, k, dtype)
+
+
+@pytest.mark.parametrize("k,n,per", [(512, 64, 2), (512, 200, 40), (512, 300, 200), (96, 40, 20), (512, 8192, 100),
+                                     (384, 8191, 400), (96, 300, 100)])
 def test_linear_leaves_rows_outside_the_offsets(L, k, n, per):
     # rows before the first offset and behind the last stay as they were, and a strided out keeps its gaps
     counts = [per, 0, per + 3]
@@ -241,9 +271,9 @@ def test_linear_leaves_rows_outside_the_offsets(L, k, n, per):
     assert (whole == 7.25).all()
 
 
-@pytest.mark.parametrize("rows,k", [(4, 512), (100, 512), (4, 96), (600, 1024)])
+@pytest.mark.parametrize("rows,k", [(4, 512), (100, 512), (4, 96), (600, 1024), (3000, 640)])
 def test_linear_offsets_out_of_range_stay_inside(L, rows, k):
-    n = 40
+    n = 40 if rows < 3000 else 2000
     ac, asc = random_mx4((rows,), k, 31)
     wc, wsc = random_mx4((4, n), k, 32)
     guard = torch.full((rows + 64, n), 3.5, device="cuda")
@@ -258,7 +288,8 @@ def test_linear_offsets_out_of_range_stay_inside(L, rows, k):
     assert (guard[rows:] == 3.5).all()
 
 
-@pytest.mark.parametrize("rows,k,n", [(3, 512, 40), (80, 512, 300), (300, 1024, 300), (3, 96, 40), (300, 128, 260)])
+@pytest.mark.parametrize("rows,k,n", [(3, 512, 40), (80, 512, 300), (300, 1024, 300), (3, 96, 40), (300, 128, 260),
+                                      (600, 1024, 8192), (2048, 384, 8192)])
 def test_linear_nan_scales(L, rows, k, n):
     # a NaN block of a row poisons that row alone, one of a weight row that column alone
     ac, asc = random_mx4((rows,), k, 41)
@@ -274,7 +305,8 @@ def test_linear_nan_scales(L, rows, k, n):
     assert_linear(got.nan_to_num(0.0), np.where(nan, 0, y), mag, k, "fp32")
 
 
-@pytest.mark.parametrize("rows,k,n", [(2, 512, 20), (40, 512, 256), (300, 512, 256), (2, 128, 20)])
+@pytest.mark.parametrize("rows,k,n", [(2, 512, 20), (40, 512, 256), (300, 512, 256), (2, 128, 20), (600, 512, 8192),
+                                      (600, 96, 300)])
 def test_linear_extreme_scales(L, rows, k, n):
     # 2^-127 and large scales meet: products inside fp32's range are right
     ac, asc = random_mx4((rows,), k, 51)
@@ -298,9 +330,10 @@ def test_linear_of_slices_and_copies(L):
     assert_linear(got, y, mag, k, "fp32")
 
 
-def test_linear_unaligned_scales(L):
+@pytest.mark.parametrize("rows,n", [(20, 40), (700, 4096)])
+def test_linear_unaligned_scales(L, rows, n):
     # scale bytes that start one byte off: the loads go by the alignment
-    k, n, rows = 1024, 40, 20
+    k = 1024
     ac, asc = random_mx4((rows,), k, 63)
     wc, wsc = random_mx4((1, n), k, 64)
     c = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
@@ -323,7 +356,8 @@ def test_linear_empty(L):
     assert (out == 2.5).all()
 
 
-@pytest.mark.parametrize("rows,n,k,mats", [(1, 256, 1024, 1), (64, 300, 1024, 3), (700, 512, 2048, 2)])
+@pytest.mark.parametrize("rows,n,k,mats", [(1, 256, 1024, 1), (64, 300, 1024, 3), (700, 512, 2048, 2), (900, 4096, 1024, 3),
+                                           (2500, 8192, 512, 2)])
 def test_quantize_and_linear_in_a_replayed_graph(L, rows, n, k, mats):
     # captured once, replayed with new inputs between eager calls of the same
     g = torch.Generator(device="cuda").manual_seed(7)
@@ -349,9 +383,9 @@ def test_quantize_and_linear_in_a_replayed_graph(L, rows, n, k, mats):
         assert torch.equal(got, call())
 
 
-@pytest.mark.parametrize("rows", [2, 40, 600])
+@pytest.mark.parametrize("rows", [2, 40, 600, 2100])
 def test_linear_on_two_streams(L, rows):
-    k, n = 1024, 512
+    k, n = 1024, 512 if rows < 600 else 8192
     c = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
     sets = []
     for i in range(2):
