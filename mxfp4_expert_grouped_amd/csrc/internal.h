@@ -193,12 +193,11 @@ hipError_t launch_linear_mx4(const LinearArgs& a, RowType dt, hipStream_t st);
 
 // pairs sorted by one workgroup in one launch
 constexpr int kSortSmallPairs = 4096;
-// pairs per workgroup above that: at least 2048, and at most 512 chunks, so
-// that summing the counts along the chunks stays short
-inline int sort_chunk(int64_t pairs) {
-  const int64_t c = (pairs + 511) / 512;
-  return static_cast<int>(std::max<int64_t>(2048, (c + 1023) / 1024 * 1024));
-}
+// pairs per workgroup above that: at most kSortSmallPairs, and half of them
+// while that fills the chip better
+inline int sort_chunk(int64_t pairs) { return pairs <= (int64_t(1) << 20) ? kSortSmallPairs / 2 : kSortSmallPairs; }
+// chunks up to which every ranking workgroup sums all chunks' counts itself
+constexpr int kSortFusedChunks = 128;
 hipError_t launch_sort_tokens(const void* ids, bool ids64, int64_t pairs, int E, int* offsets, int* row_src,
                               int* token_row, int* counts, hipStream_t st);
 hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t ld_x, const int* token_row, int64_t T, int k,

@@ -16,17 +16,26 @@
 namespace mxmoe {
 
 // ---------------------------------------------------------------------------
-// Sorting.  A workgroup of 16 waves ranks a chunk of pairs: wave w takes the
-// w-th sixteenth of it, 64 pairs at a time.  Lanes with equal keys find each
-// other by one ballot per key bit; the number of equal lanes below is a pair's
-// rank among the 64, and the first lane of each key adds their number to the
-// wave's own count of that key in LDS.  No atomics: equal keys keep the order
-// of their pairs, and a token that names an expert twice has two rows.
-// Up to kSortSmall pairs one workgroup does everything in one launch; above
-// it, the chunks are counted, the counts summed along the chunks by one
-// workgroup (a thread per expert), and the chunks ranked again and written.
+// Sorting.  A workgroup of 16 waves ranks at most 4096 pairs: a wave takes a
+// contiguous stretch of them, 64 pairs at a time, at most four times, and
+// keeps their keys in registers.  Lanes with equal keys find each other by one
+// ballot per key bit; the number of equal lanes below is a pair's rank among
+// the 64, and the first lane of each key adds their number to the wave's own
+// count of that key in LDS.  No atomics: equal keys keep the order of their
+// pairs, and a token that names an expert twice has two rows.
+//
+// Bound by the latency of its few steps, so their number is kept low: up to
+// kSortSmallPairs everything is one launch of one workgroup (256 tokens, top
+// 16 of 896: 11.9 us when every pass loaded the ids again and the waves'
+// counts were summed one after the other, 9.8 us now; one token 4.3 us).  Above it a first launch
+// counts the keys of every chunk, and each ranking workgroup sums those of the
+// chunks before its own and of all (131072 pairs, 64 chunks: two launches of
+// together 16 us; with a workgroup of its own that summed, 24 us).  Above
+// kSortFusedChunks chunks that reading would grow with their square, and a
+// launch between the two sums them.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortBatches = kSortSmallPairs / kSortThreads;  // of 64 pairs, per wave
 constexpr int kMaxExperts = 1024;
 
 template <typename I>
@@ -35,15 +44,18 @@ __device__ __forceinline__ int sort_key(const I* ids, int p, int E) {
   return v >= 0 && v < E ? static_cast<int>(v) : -1;
 }
 
-// lanes of the wave with this lane's key (valid lanes only)
+// Lanes of the wave with this lane's key (valid lanes only): per key bit those
+// with the same bit, m & ~(ballot ^ the bit in all places).
 __device__ __forceinline__ uint64_t equal_lanes(int key, int bits) {
-  uint64_t m = __ballot(key >= 0);
+  const uint64_t valid = __ballot(key >= 0);
+  uint32_t lo = static_cast<uint32_t>(valid), hi = static_cast<uint32_t>(valid >> 32);
   for (int b = 0; b < bits; ++b) {
-    const bool one = (key >> b) & 1;
-    const uint64_t s = __ballot(one);
-    m &= one ? s : ~s;
+    const uint32_t bit = static_cast<uint32_t>(__builtin_amdgcn_sbfe(key, b, 1));
+    const uint64_t s = __ballot(bit != 0);
+    lo &= ~(static_cast<uint32_t>(s) ^ bit);
+    hi &= ~(static_cast<uint32_t>(s >> 32) ^ bit);
   }
-  return m;
+  return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
 __device__ __forceinline__ int lanes_below(uint64_t m) {
@@ -74,72 +86,95 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int& total) {
   return before + inc - v;
 }
 
-// One wave's pass over its pairs [lo, hi): f(pair, key, rank among equals in
-// this batch, first lane of its key, lanes of its key)
-template <typename I, typename F>
-__device__ __forceinline__ void each_batch(const I* ids, int lo, int hi, int E, int bits, F f) {
-  const int lane = threadIdx.x & 63;
-  for (int at = lo; at < hi; at += 64) {
-    const int p = at + lane;
-    const int key = p < hi ? sort_key(ids, p, E) : -1;
-    const uint64_t eq = equal_lanes(key, bits);
-    const int rank = lanes_below(eq);
-    f(p, key, rank, rank == 0, __popcll(eq));
-  }
-}
+// How the pairs outside a workgroup's chunk come in.  kAlone: there are none.
+// kCounts: `table` has every chunk's count of every expert, [chunks][E].
+// kBases: `table` has the first row of every (chunk, expert).
+enum SortTable { kAlone, kCounts, kBases };
 
-// Whole sort (SMALL) or one chunk's part of it.  base: first row of each
-// (expert, chunk), [chunks][E], when not SMALL.
-template <typename I, bool SMALL>
+template <typename I, SortTable TABLE>
 __global__ void __launch_bounds__(kSortThreads) k_sort_rank(const I* __restrict__ ids, int P, int E, int bits, int chunk,
-                                                            const int* __restrict__ base, int* __restrict__ offsets,
+                                                            const int* __restrict__ table, int* __restrict__ offsets,
                                                             int* __restrict__ row_src, int* __restrict__ token_row) {
   __shared__ int cnt[kSortWaves * kMaxExperts];
   __shared__ int part[kSortWaves];
-  const int tid = threadIdx.x, wave = tid >> 6;
-  const int c0 = SMALL ? 0 : blockIdx.x * chunk;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c0 = TABLE == kAlone ? 0 : blockIdx.x * chunk;
   const int n = min(chunk, P - c0);
-  const int per = (((n + kSortWaves - 1) / kSortWaves) + 63) & ~63;
-  const int lo = c0 + min(n, wave * per), hi = c0 + min(n, (wave + 1) * per);
+  // batches per wave, and waves that have any
+  const int per = (n + kSortThreads - 1) / kSortThreads;
+  const int waves = per ? (n + 64 * per - 1) / (64 * per) : 0;
+  int key[kSortBatches];
+#pragma unroll
+  for (int b = 0; b < kSortBatches; ++b) {
+    const int i = (wave * per + b) * 64 + lane;
+    key[b] = b < per && i < n ? sort_key(ids, c0 + i, E) : -1;
+  }
+  int before = 0, total = 0;   // of this thread's expert: rows in earlier chunks, in all (kCounts)
+  if (TABLE == kCounts && tid < E) {
+    // 32 loads on their way at a time
+    const int chunks = gridDim.x;
+    for (int c = 0; c < chunks; c += 32) {
+      int v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = c + i < chunks ? table[(c + i) * E + tid] : 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        total += v[i];
+        before += c + i < static_cast<int>(blockIdx.x) ? v[i] : 0;
+      }
+    }
+  }
   // volatile: a lane reads counts that other lanes of its wave have moved on
   volatile int* mine = cnt + wave * E;
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) cnt[i] = 0;
+  for (int i = tid; i < waves * E; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
-  each_batch(ids, lo, hi, E, bits, [&](int, int key, int, bool first, int same) {
-    if (key >= 0 && first) mine[key] = mine[key] + same;
-  });
+  uint64_t equal[kSortBatches];
+#pragma unroll
+  for (int b = 0; b < kSortBatches; ++b) {
+    if (b >= per || wave >= waves) break;
+    equal[b] = equal_lanes(key[b], bits);
+    if (key[b] >= 0 && lanes_below(equal[b]) == 0) mine[key[b]] = mine[key[b]] + __popcll(equal[b]);
+  }
   __syncthreads();
   int rows;   // rows in all
   {
-    int sum = 0;
-    if (tid < E)
-      for (int w = 0; w < kSortWaves; ++w) {
-        const int c = cnt[w * E + tid];
-        cnt[w * E + tid] = sum;
-        sum += c;
-      }
+    int c[kSortWaves], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = tid < E && w < waves ? cnt[w * E + tid] : 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) sum += c[w];
     int from;
-    if (SMALL) {
-      from = block_exclusive(sum, part, rows);
-      if (tid < E) offsets[tid] = from;
-      if (tid == 0) offsets[E] = rows;
-    } else {
-      from = tid < E ? base[int64_t(blockIdx.x) * E + tid] : 0;
+    if (TABLE == kBases) {
+      from = tid < E ? table[int64_t(blockIdx.x) * E + tid] : 0;
       rows = offsets[E];
+    } else {
+      from = block_exclusive(TABLE == kAlone ? sum : total, part, rows);
+      if (blockIdx.x == 0) {
+        if (tid < E) offsets[tid] = from;
+        if (tid == 0) offsets[E] = rows;
+      }
+      from += before;
     }
-    if (tid < E)
-      for (int w = 0; w < kSortWaves; ++w) cnt[w * E + tid] += from;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      if (tid < E && w < waves) cnt[w * E + tid] = from;
+      from += c[w];
+    }
   }
   __syncthreads();
-  each_batch(ids, lo, hi, E, bits, [&](int p, int key, int rank, bool first, int same) {
-    const int row = key >= 0 ? mine[key] + rank : -1;
+#pragma unroll
+  for (int b = 0; b < kSortBatches; ++b) {
+    if (b >= per || wave >= waves) break;
+    const int i = (wave * per + b) * 64 + lane;
+    const int rank = key[b] >= 0 ? lanes_below(equal[b]) : 0;
+    const int row = key[b] >= 0 ? mine[key[b]] + rank : -1;
     // every lane has read its key's count before the first one moves it on
     __builtin_amdgcn_wave_barrier();
-    if (key >= 0 && first) mine[key] = row + same;
-    if (key >= 0) row_src[row] = p;
-    if (p < hi) token_row[p] = row;
+    if (key[b] >= 0 && rank == 0) mine[key[b]] = row + __popcll(equal[b]);
+    if (key[b] >= 0) row_src[row] = c0 + i;
+    if (i < n) token_row[c0 + i] = row;
     __builtin_amdgcn_wave_barrier();
-  });
+  }
   // entries of this chunk's range behind the last row
   for (int i = max(c0, rows) + tid; i < c0 + n; i += kSortThreads) row_src[i] = -1;
 }
@@ -167,18 +202,22 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scan(int* __restrict__ co
   const int e = threadIdx.x;
   int sum = 0;
   if (e < E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int c = 0; c < chunks; ++c) sum += counts[int64_t(c) * E + e];
   }
   int rows;
   int at = block_exclusive(sum, part, rows);
   if (e < E) {
     offsets[e] = at;
-#pragma unroll 8
-    for (int c = 0; c < chunks; ++c) {
-      const int n = counts[int64_t(c) * E + e];
-      counts[int64_t(c) * E + e] = at;
-      at += n;
+    for (int c = 0; c < chunks; c += 16) {
+      int n[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) n[i] = c + i < chunks ? counts[int64_t(c + i) * E + e] : 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (c + i < chunks) counts[int64_t(c + i) * E + e] = at;
+        at += n[i];
+      }
     }
   }
   if (e == 0) offsets[E] = rows;
@@ -193,13 +232,17 @@ hipError_t sort_t(const I* ids, int64_t pairs, int E, int* offsets, int* row_src
   int bits = 0;
   while ((1 << bits) < E) ++bits;
   if (pairs <= kSortSmallPairs) {
-    k_sort_rank<I, true><<<1, kSortThreads, 0, st>>>(ids, P, E, bits, P, nullptr, offsets, row_src, token_row);
+    k_sort_rank<I, kAlone><<<1, kSortThreads, 0, st>>>(ids, P, E, bits, P, nullptr, offsets, row_src, token_row);
     return hipGetLastError();
   }
   const int chunk = sort_chunk(pairs), chunks = (P + chunk - 1) / chunk;
   k_sort_count<I><<<chunks, kSortThreads, 0, st>>>(ids, P, E, chunk, counts);
-  k_sort_scan<<<1, kSortThreads, 0, st>>>(counts, chunks, E, offsets);
-  k_sort_rank<I, false><<<chunks, kSortThreads, 0, st>>>(ids, P, E, bits, chunk, counts, offsets, row_src, token_row);
+  if (chunks > kSortFusedChunks) {
+    k_sort_scan<<<1, kSortThreads, 0, st>>>(counts, chunks, E, offsets);
+    k_sort_rank<I, kBases><<<chunks, kSortThreads, 0, st>>>(ids, P, E, bits, chunk, counts, offsets, row_src, token_row);
+  } else {
+    k_sort_rank<I, kCounts><<<chunks, kSortThreads, 0, st>>>(ids, P, E, bits, chunk, counts, offsets, row_src, token_row);
+  }
   return hipGetLastError();
 }
 
@@ -214,7 +257,8 @@ hipError_t launch_sort_tokens(const void* ids, bool ids64, int64_t pairs, int E,
 // ---------------------------------------------------------------------------
 // Dispatch: every token's row to the rows of its pairs.  A workgroup takes a
 // token's row once (or one of `splits` stretches of it) and writes each copy,
-// so x is read once from memory.  Element-agnostic: V is the widest word that
+// so x is read once from memory (8192 tokens, top 16, 7168 bf16: 380 us, 5.3
+// TB/s, of which 16/17 are the copies; no hint on them gained).  Element-agnostic: V is the widest word that
 // rows and strides are aligned to.  num_rows (may be null): the same
 // workgroup zero-fills its share of the rows from *num_rows on.
 // ---------------------------------------------------------------------------
@@ -285,32 +329,31 @@ hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t ld_x, 
 // Combine: y[t] = sum over j ascending of w[t,j] rows[token_row[t,j]] in fp32,
 // rounded once; dropped pairs are neither read nor added.  A thread holds VEC
 // columns (16 bytes) of one token; the loop over the pairs starts kAhead rows'
-// loads before it adds the first.
+// loads before it adds the first.  Bound by reading the rows once: 131072 x
+// 7168 bf16 373 us (5.4 TB/s; 400 with kAhead = 8, 547 with 16), 65520 x 7168
+// fp32 362 us; NT, the non-temporal hint for rows and result, is for more rows
+// than a cache keeps (454 and 421 us without it).
 // ---------------------------------------------------------------------------
 constexpr int kAhead = 4;
 
-template <typename T, int VEC>
-struct Piece {
-  float v[VEC];
-};
-
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void load_piece(const T* p, float* v) {
   if constexpr (VEC == 1) v[0] = to_f32(*p);
-  else if constexpr (VEC == 8) load8<T, true>(p, v);
+  else if constexpr (VEC == 8) load8<T, true, NT>(p, v);
   else {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    const f32x4 a = load16<NT, f32x4>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i];
   }
 }
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void store_piece(T* p, const float* v) {
   if constexpr (VEC == 1) *p = from_f32<T>(v[0]);
-  else if constexpr (VEC == 8) store8<T, true>(p, v);
-  else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (VEC == 8) store8<T, true, NT>(p, v);
+  else store16<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT>
 __global__ void __launch_bounds__(kRowThreads) k_combine_rows(const T* __restrict__ rows, int64_t ld, int64_t R,
                                                               const int* __restrict__ token_row,
                                                               const float* __restrict__ w, int k, int64_t pieces,
@@ -326,30 +369,32 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_rows(const T* __restric
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < k; j0 += kAhead) {
-      Piece<T, VEC> v[kAhead];
+      float v[kAhead][VEC];
       bool there[kAhead];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         const int64_t r = j0 + a < k ? tr[j0 + a] : -1;
         there[a] = r >= 0 && r < R;
-        if (there[a]) load_piece<T, VEC>(rows + r * ld + c * VEC, v[a].v);
+        if (there[a]) load_piece<T, VEC, NT>(rows + r * ld + c * VEC, v[a]);
       }
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         if (!there[a]) continue;
         const float f = wt ? wt[j0 + a] : 1.0f;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(f, v[a].v[i], acc[i]);
+        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(f, v[a][i], acc[i]);
       }
     }
-    store_piece<T, VEC>(y + t * ld_y + c * VEC, acc);
+    store_piece<T, VEC, NT>(y + t * ld_y + c * VEC, acc);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Gradients of combine: a wave per pair reads its row and the token's dy once,
 // drows = w dy (rounded once) and dw = <dy, row> in fp32, lane sums joined by
-// a butterfly (a fixed order).  A dropped pair has dw = 0.  num_rows (may be
+// a butterfly (a fixed order).  Bound by memory: 65520 x 7168 fp32 754 us (5.1
+// TB/s; 925 with the non-temporal hint, as a token's waves share its dy).  A
+// dropped pair has dw = 0.  num_rows (may be
 // null): the wave of pair p also zero-fills the rows p, p + T*k, ... of drows
 // from *num_rows on.
 // ---------------------------------------------------------------------------
@@ -413,7 +458,9 @@ template <typename T, int VEC>
 hipError_t combine_v(const CombineArgs& a, hipStream_t st) {
   const int64_t pieces = a.d / VEC;
   const int splits = row_splits(a.T, (pieces + kRowThreads - 1) / kRowThreads);
-  k_combine_rows<T, VEC><<<static_cast<unsigned>(a.T * splits), kRowThreads, 0, st>>>(
+  const bool nt = VEC > 1 && a.T * a.k * a.d * int64_t(sizeof(T)) >= kStreamedBytes;
+  auto* k = nt ? k_combine_rows<T, VEC, (VEC > 1)> : k_combine_rows<T, VEC, false>;
+  k<<<static_cast<unsigned>(a.T * splits), kRowThreads, 0, st>>>(
       static_cast<const T*>(a.rows), a.ld, a.R, a.token_row, a.w, a.k, pieces, static_cast<T*>(a.y), a.ld_y, splits);
   return hipGetLastError();
 }

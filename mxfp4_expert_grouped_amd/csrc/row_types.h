@@ -36,37 +36,57 @@ __device__ __forceinline__ void unpack2<_Float16>(uint32_t w, float& a, float& b
   b = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w >> 16)));
 }
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes, with the non-temporal hint or without
+template <bool NT, typename V>
+__device__ __forceinline__ V load16(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  else return *static_cast<const V*>(p);
+}
+template <bool NT, typename V>
+__device__ __forceinline__ void store16(void* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else *static_cast<V*>(p) = v;
+}
+
 // eight consecutive elements; ALIGNED: p is on 16 bytes
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, bool NT = false>
 __device__ __forceinline__ void load8(const T* p, float* v) {
   if constexpr (!ALIGNED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
   } else if constexpr (sizeof(T) == 4) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const f32x4 a = load16<NT, f32x4>(p), b = load16<NT, f32x4>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    unpack2<T>(a.x, v[0], v[1]);
-    unpack2<T>(a.y, v[2], v[3]);
-    unpack2<T>(a.z, v[4], v[5]);
-    unpack2<T>(a.w, v[6], v[7]);
+    const u32x4 a = load16<NT, u32x4>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2<T>(a[i], v[2 * i], v[2 * i + 1]);
   }
 }
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, bool NT = false>
 __device__ __forceinline__ void store8(T* p, const float* v) {
   if constexpr (!ALIGNED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = from_f32<T>(v[i]);
   } else if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    store16<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
+    store16<NT>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
   } else {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+    store16<NT>(p, u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])});
   }
 }
+
+// Bytes from which on an operand that is read once is read with the
+// non-temporal hint: more of it than a part of the 256 MB Infinity Cache would
+// not be found there again.
+constexpr int64_t kStreamedBytes = int64_t(64) << 20;
 
 // whether every row of a matrix starts on `a` bytes
 inline bool rows_aligned(const void* p, int64_t ld_bytes, int64_t a) {

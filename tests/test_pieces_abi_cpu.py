@@ -87,7 +87,7 @@ def test_sort_tokens_workspace(M):
     assert M.moe_sort_tokens_workspace_bytes(0, 1, 1) == 0
     assert M.moe_sort_tokens_workspace_bytes(1, 32, 1024) == 0
     big = M.moe_sort_tokens_workspace_bytes(1 << 20, 32, 1024)
-    assert 0 < M.moe_sort_tokens_workspace_bytes(8192, 16, 896) <= big <= 512 * 1024 * 4
+    assert 0 < M.moe_sort_tokens_workspace_bytes(8192, 16, 896) <= big <= (1 << 13) * 1024 * 4
     for bad in ((-1, 1, 1), (1, 0, 1), (1, 33, 1), (1, 1, 0), (1, 1, 1025), ((1 << 20) + 1, 1, 1)):
         with pytest.raises(M.MoeError):
             M.moe_sort_tokens_workspace_bytes(*bad)
