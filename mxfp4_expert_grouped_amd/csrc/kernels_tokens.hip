@@ -258,37 +258,49 @@ hipError_t launch_sort_tokens(const void* ids, bool ids64, int64_t pairs, int E,
 // Dispatch: every token's row to the rows of its pairs.  A workgroup takes a
 // token's row once (or one of `splits` stretches of it) and writes each copy,
 // so x is read once from memory (8192 tokens, top 16, 7168 bf16: 380 us, 5.3
-// TB/s, of which 16/17 are the copies; no hint on them gained).  Element-agnostic: V is the widest word that
-// rows and strides are aligned to.  num_rows (may be null): the same
-// workgroup zero-fills its share of the rows from *num_rows on.
+// TB/s, of which 16/17 are the copies; no hint on them gained).  Bytes whatever
+// the elements: 16 at a time, ALIGNED if rows start on 16 bytes, and the last
+// few one by one.  num_rows (may be null): the same workgroup zero-fills its
+// share of the rows from *num_rows on.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 
-template <typename V>
-__global__ void __launch_bounds__(kRowThreads) k_dispatch(const char* __restrict__ x, int64_t ld_x, int64_t row_words,
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kRowThreads) k_dispatch(const char* __restrict__ x, int64_t ld_x, int64_t row_bytes,
                                                           const int* __restrict__ token_row, int k, int64_t T,
                                                           int64_t R, const int* __restrict__ num_rows,
                                                           char* __restrict__ out, int64_t ld_out, int splits) {
   const int64_t t = blockIdx.x / splits;
   const int s = blockIdx.x - static_cast<int>(t * splits);
-  const int64_t per = (row_words + splits - 1) / splits;
-  const int64_t c0 = s * per, c1 = min(row_words, c0 + per);
+  const int64_t words = row_bytes / 16, per = (words + splits - 1) / splits;
+  const int64_t c0 = s * per, c1 = min(words, c0 + per);
+  // the last stretch's first threads take the bytes behind the last word
+  const int64_t tail = 16 * words + threadIdx.x;
+  const bool has_tail = s == splits - 1 && tail < row_bytes;
   const int* tr = token_row + t * k;
-  const V* src = reinterpret_cast<const V*>(x + t * ld_x);
+  const char* src = x + t * ld_x;
   for (int64_t c = c0 + threadIdx.x; c < c1; c += kRowThreads) {
-    const V v = src[c];
+    const u32x4 v = load16<ALIGNED, false, u32x4>(src + 16 * c);
     for (int j = 0; j < k; ++j) {
       const int64_t r = tr[j];
-      if (r >= 0 && r < R) reinterpret_cast<V*>(out + r * ld_out)[c] = v;
+      if (r >= 0 && r < R) store16<ALIGNED, false>(out + r * ld_out + 16 * c, v);
     }
   }
+  if (has_tail)
+    for (int j = 0; j < k; ++j) {
+      const int64_t r = tr[j];
+      if (r >= 0 && r < R) out[r * ld_out + tail] = src[tail];
+    }
   if (num_rows) {
     const int64_t n = max(0, *num_rows);
     // rows t, t + T, ... at or past n
     int64_t r = t;
     if (r < n) r += (n - r + T - 1) / T * T;
-    for (; r < R; r += T)
-      for (int64_t c = c0 + threadIdx.x; c < c1; c += kRowThreads) reinterpret_cast<V*>(out + r * ld_out)[c] = V{};
+    for (; r < R; r += T) {
+      for (int64_t c = c0 + threadIdx.x; c < c1; c += kRowThreads)
+        store16<ALIGNED, false>(out + r * ld_out + 16 * c, u32x4{0, 0, 0, 0});
+      if (has_tail) out[r * ld_out + tail] = 0;
+    }
   }
 }
 
@@ -301,34 +313,21 @@ int row_splits(int64_t T, int64_t passes) {
   return static_cast<int>(std::max<int64_t>(1, s));
 }
 
-template <typename V>
-hipError_t dispatch_v(const void* x, int64_t row_bytes, int64_t ld_x, const int* token_row, int64_t T, int k, int64_t R,
-                      const int* num_rows, void* out, int64_t ld_out, hipStream_t st) {
-  const int64_t words = row_bytes / sizeof(V);
-  const int splits = row_splits(T, (words + kRowThreads - 1) / kRowThreads);
-  k_dispatch<V><<<static_cast<unsigned>(T * splits), kRowThreads, 0, st>>>(
-      static_cast<const char*>(x), ld_x, words, token_row, k, T, R, num_rows, static_cast<char*>(out), ld_out, splits);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t ld_x, const int* token_row, int64_t T, int k,
                                 int64_t R, const int* num_rows, void* out, int64_t ld_out, hipStream_t st) {
-  auto fits = [&](int64_t a) { return row_bytes % a == 0 && rows_aligned(x, ld_x, a) && rows_aligned(out, ld_out, a); };
-  auto go = [&](auto v) {
-    return dispatch_v<decltype(v)>(x, row_bytes, ld_x, token_row, T, k, R, num_rows, out, ld_out, st);
-  };
-  if (fits(16)) return go(uint4{});
-  if (fits(4)) return go(uint32_t{});
-  if (fits(2)) return go(uint16_t{});
-  return go(uint8_t{});
+  const int splits = row_splits(T, (row_bytes / 16 + kRowThreads - 1) / kRowThreads);
+  auto* go = rows_aligned(x, ld_x, 16) && rows_aligned(out, ld_out, 16) ? k_dispatch<true> : k_dispatch<false>;
+  go<<<static_cast<unsigned>(T * splits), kRowThreads, 0, st>>>(static_cast<const char*>(x), ld_x, row_bytes, token_row, k,
+                                                                T, R, num_rows, static_cast<char*>(out), ld_out, splits);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // Combine: y[t] = sum over j ascending of w[t,j] rows[token_row[t,j]] in fp32,
-// rounded once; dropped pairs are neither read nor added.  A thread holds VEC
-// columns (16 bytes) of one token; the loop over the pairs starts kAhead rows'
+// rounded once; dropped pairs are neither read nor added.  A thread holds 16
+// bytes of columns of one token; the loop over the pairs starts kAhead rows'
 // loads before it adds the first.  Bound by reading the rows once: 131072 x
 // 7168 bf16 373 us (5.4 TB/s; 400 with kAhead = 8, 547 with 16), 65520 x 7168
 // fp32 362 us; NT, the non-temporal hint for rows and result, is for more rows
@@ -336,31 +335,32 @@ hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t ld_x, 
 // ---------------------------------------------------------------------------
 constexpr int kAhead = 4;
 
-template <typename T, int VEC, bool NT = false>
-__device__ __forceinline__ void load_piece(const T* p, float* v) {
-  if constexpr (VEC == 1) v[0] = to_f32(*p);
-  else if constexpr (VEC == 8) load8<T, true, NT>(p, v);
-  else {
-    const f32x4 a = load16<NT, f32x4>(p);
+// The kVec elements of a row from column at on; of a row's last piece only
+// those before column d are there (FULL: d is a whole number of pieces and
+// rows are on 16 bytes).
+template <typename T, bool FULL, bool NT = false>
+__device__ __forceinline__ void load_piece(const T* row, int64_t at, int64_t d, float* v) {
+  if (FULL || at + kVec<T> <= d) return load_vec<T, FULL, NT>(row + at, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i];
-  }
+  for (int i = 0; i < kVec<T>; ++i) v[i] = at + i < d ? to_f32(row[at + i]) : 0.0f;
 }
-template <typename T, int VEC, bool NT = false>
-__device__ __forceinline__ void store_piece(T* p, const float* v) {
-  if constexpr (VEC == 1) *p = from_f32<T>(v[0]);
-  else if constexpr (VEC == 8) store8<T, true, NT>(p, v);
-  else store16<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
+template <typename T, bool FULL, bool NT = false>
+__device__ __forceinline__ void store_piece(T* row, int64_t at, int64_t d, const float* v) {
+  if (FULL || at + kVec<T> <= d) return store_vec<T, FULL, NT>(row + at, v);
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i)
+    if (at + i < d) row[at + i] = from_f32<T>(v[i]);
 }
 
-template <typename T, int VEC, bool NT>
+template <typename T, bool FULL, bool NT>
 __global__ void __launch_bounds__(kRowThreads) k_combine_rows(const T* __restrict__ rows, int64_t ld, int64_t R,
                                                               const int* __restrict__ token_row,
-                                                              const float* __restrict__ w, int k, int64_t pieces,
+                                                              const float* __restrict__ w, int k, int64_t d,
                                                               T* __restrict__ y, int64_t ld_y, int splits) {
+  constexpr int VEC = kVec<T>;
   const int64_t t = blockIdx.x / splits;
   const int s = blockIdx.x - static_cast<int>(t * splits);
-  const int64_t per = (pieces + splits - 1) / splits;
+  const int64_t pieces = (d + VEC - 1) / VEC, per = (pieces + splits - 1) / splits;
   const int64_t c0 = s * per, c1 = min(pieces, c0 + per);
   const int* tr = token_row + t * k;
   const float* wt = w ? w + t * k : nullptr;
@@ -369,23 +369,26 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_rows(const T* __restric
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < k; j0 += kAhead) {
-      float v[kAhead][VEC];
-      bool there[kAhead];
+      // row numbers and weights first, then the rows: one wait for each
+      int r[kAhead];
+      float f[kAhead], v[kAhead][VEC];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        const int64_t r = j0 + a < k ? tr[j0 + a] : -1;
-        there[a] = r >= 0 && r < R;
-        if (there[a]) load_piece<T, VEC, NT>(rows + r * ld + c * VEC, v[a]);
+        const bool in = j0 + a < k;
+        r[a] = in ? tr[j0 + a] : -1;
+        f[a] = wt && in ? wt[j0 + a] : 1.0f;
       }
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        if (!there[a]) continue;
-        const float f = wt ? wt[j0 + a] : 1.0f;
+      for (int a = 0; a < kAhead; ++a)
+        if (r[a] >= 0 && r[a] < R) load_piece<T, FULL, NT>(rows + r[a] * ld, c * VEC, d, v[a]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(f, v[a][i], acc[i]);
+      for (int a = 0; a < kAhead; ++a) {
+        if (r[a] < 0 || r[a] >= R) continue;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(f[a], v[a][i], acc[i]);
       }
     }
-    store_piece<T, VEC, NT>(y + t * ld_y + c * VEC, acc);
+    store_piece<T, FULL, NT>(y + t * ld_y, c * VEC, d, acc);
   }
 }
 
@@ -398,20 +401,21 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_rows(const T* __restric
 // null): the wave of pair p also zero-fills the rows p, p + T*k, ... of drows
 // from *num_rows on.
 // ---------------------------------------------------------------------------
-template <typename T, int VEC>
+template <typename T, bool FULL>
 __global__ void __launch_bounds__(kRowThreads) k_combine_bwd(const T* __restrict__ dy, int64_t ld_dy,
                                                              const T* __restrict__ rows, int64_t ld, int64_t R,
                                                              const int* __restrict__ token_row,
                                                              const float* __restrict__ w, int k, int64_t P,
-                                                             int64_t pieces, const int* __restrict__ num_rows,
+                                                             int64_t d, const int* __restrict__ num_rows,
                                                              T* __restrict__ drows, int64_t ld_d, float* __restrict__ dw) {
+  constexpr int VEC = kVec<T>;
   const int lane = threadIdx.x & 63;
   const int64_t p = int64_t(blockIdx.x) * (kRowThreads / 64) + (threadIdx.x >> 6);
   if (p >= P) return;
+  const int64_t pieces = (d + VEC - 1) / VEC;
   const int64_t r = token_row[p];
-  const bool there = r >= 0 && r < R;
-  if (there) {
-    const T* d = dy + (p / k) * ld_dy;
+  if (r >= 0 && r < R) {
+    const T* g_row = dy + (p / k) * ld_dy;
     const T* row = rows + r * ld;
     T* out = drows ? drows + r * ld_d : nullptr;
     const float f = w ? w[p] : 1.0f;
@@ -419,17 +423,17 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_bwd(const T* __restrict
 #pragma unroll 4
     for (int64_t c = lane; c < pieces; c += 64) {
       float g[VEC];
-      load_piece<T, VEC>(d + c * VEC, g);
+      load_piece<T, FULL>(g_row, c * VEC, d, g);
       if (dw) {
         float v[VEC];
-        load_piece<T, VEC>(row + c * VEC, v);
+        load_piece<T, FULL>(row, c * VEC, d, v);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) sum = fmaf(g[i], v[i], sum);
       }
       if (out) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) g[i] *= f;
-        store_piece<T, VEC>(out + c * VEC, g);
+        store_piece<T, FULL>(out, c * VEC, d, g);
       }
     }
     if (dw) {
@@ -448,46 +452,39 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_bwd(const T* __restrict
     int64_t q = p;
     if (q < n) q += (n - q + P - 1) / P * P;
     for (; q < R; q += P)
-      for (int64_t c = lane; c < pieces; c += 64) store_piece<T, VEC>(drows + q * ld_d + c * VEC, zero);
+      for (int64_t c = lane; c < pieces; c += 64) store_piece<T, FULL>(drows + q * ld_d, c * VEC, d, zero);
   }
 }
 
 namespace {
 
-template <typename T, int VEC>
-hipError_t combine_v(const CombineArgs& a, hipStream_t st) {
-  const int64_t pieces = a.d / VEC;
-  const int splits = row_splits(a.T, (pieces + kRowThreads - 1) / kRowThreads);
-  const bool nt = VEC > 1 && a.T * a.k * a.d * int64_t(sizeof(T)) >= kStreamedBytes;
-  auto* k = nt ? k_combine_rows<T, VEC, (VEC > 1)> : k_combine_rows<T, VEC, false>;
-  k<<<static_cast<unsigned>(a.T * splits), kRowThreads, 0, st>>>(
-      static_cast<const T*>(a.rows), a.ld, a.R, a.token_row, a.w, a.k, pieces, static_cast<T*>(a.y), a.ld_y, splits);
-  return hipGetLastError();
-}
-
-template <typename T, int VEC>
-hipError_t combine_bwd_v(const CombineArgs& a, hipStream_t st) {
-  const int64_t P = a.T * a.k, per = kRowThreads / 64;
-  k_combine_bwd<T, VEC><<<static_cast<unsigned>((P + per - 1) / per), kRowThreads, 0, st>>>(
-      static_cast<const T*>(a.dy), a.ld_y, static_cast<const T*>(a.rows), a.ld, a.R, a.token_row, a.w, a.k, P, a.d / VEC,
-      a.num_rows, static_cast<T*>(a.drows), a.ld_d, a.dw);
-  return hipGetLastError();
-}
-
-// 16-byte pieces where every row allows them, else single elements
+// whole 16-byte pieces at 16-byte addresses in every row
 template <typename T>
-bool wide_rows(const CombineArgs& a, const void* extra, int64_t ld_extra) {
+bool full_rows(const CombineArgs& a, const void* extra, int64_t ld_extra) {
   auto ok = [&](const void* p, int64_t ld) { return !p || rows_aligned(p, ld * sizeof(T), 16); };
-  return a.d % (16 / int64_t(sizeof(T))) == 0 && ok(a.rows, a.ld) && ok(extra, ld_extra) && ok(a.drows, a.ld_d);
+  return a.d % kVec<T> == 0 && ok(a.rows, a.ld) && ok(extra, ld_extra) && ok(a.drows, a.ld_d);
 }
 
 template <typename T>
 hipError_t combine_t(const CombineArgs& a, hipStream_t st) {
-  return wide_rows<T>(a, a.y, a.ld_y) ? combine_v<T, 16 / sizeof(T)>(a, st) : combine_v<T, 1>(a, st);
+  const int64_t pieces = (a.d + kVec<T> - 1) / kVec<T>;
+  const int splits = row_splits(a.T, (pieces + kRowThreads - 1) / kRowThreads);
+  auto* go = !full_rows<T>(a, a.y, a.ld_y) ? k_combine_rows<T, false, false>
+             : a.T * a.k * a.d * int64_t(sizeof(T)) >= kStreamedBytes ? k_combine_rows<T, true, true>
+                                                                      : k_combine_rows<T, true, false>;
+  go<<<static_cast<unsigned>(a.T * splits), kRowThreads, 0, st>>>(static_cast<const T*>(a.rows), a.ld, a.R, a.token_row, a.w,
+                                                                  a.k, a.d, static_cast<T*>(a.y), a.ld_y, splits);
+  return hipGetLastError();
 }
+
 template <typename T>
 hipError_t combine_bwd_t(const CombineArgs& a, hipStream_t st) {
-  return wide_rows<T>(a, a.dy, a.ld_y) ? combine_bwd_v<T, 16 / sizeof(T)>(a, st) : combine_bwd_v<T, 1>(a, st);
+  const int64_t P = a.T * a.k, per = kRowThreads / 64;
+  auto* go = full_rows<T>(a, a.dy, a.ld_y) ? k_combine_bwd<T, true> : k_combine_bwd<T, false>;
+  go<<<static_cast<unsigned>((P + per - 1) / per), kRowThreads, 0, st>>>(
+      static_cast<const T*>(a.dy), a.ld_y, static_cast<const T*>(a.rows), a.ld, a.R, a.token_row, a.w, a.k, P, a.d,
+      a.num_rows, static_cast<T*>(a.drows), a.ld_d, a.dw);
+  return hipGetLastError();
 }
 
 }  // namespace

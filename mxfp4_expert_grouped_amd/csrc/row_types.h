@@ -39,48 +39,55 @@ __device__ __forceinline__ void unpack2<_Float16>(uint32_t w, float& a, float& b
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// 16 bytes, with the non-temporal hint or without
-template <bool NT, typename V>
+// 16 bytes at p, which is on 16 bytes (ALIGNED) or anywhere (the target reads
+// and writes unaligned memory); with the non-temporal hint or without.
+template <bool ALIGNED, bool NT, typename V>
 __device__ __forceinline__ V load16(const void* p) {
-  if constexpr (NT) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  typedef V U __attribute__((aligned(1)));
+  if constexpr (!ALIGNED) return *static_cast<const U*>(p);
+  else if constexpr (NT) return __builtin_nontemporal_load(static_cast<const V*>(p));
   else return *static_cast<const V*>(p);
 }
-template <bool NT, typename V>
+template <bool ALIGNED, bool NT, typename V>
 __device__ __forceinline__ void store16(void* p, V v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  typedef V U __attribute__((aligned(1)));
+  if constexpr (!ALIGNED) *static_cast<U*>(p) = v;
+  else if constexpr (NT) __builtin_nontemporal_store(v, static_cast<V*>(p));
   else *static_cast<V*>(p) = v;
 }
 
-// eight consecutive elements; ALIGNED: p is on 16 bytes
+// 16 bytes of elements
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);
 template <typename T, bool ALIGNED, bool NT = false>
-__device__ __forceinline__ void load8(const T* p, float* v) {
-  if constexpr (!ALIGNED) {
+__device__ __forceinline__ void load_vec(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    const f32x4 a = load16<ALIGNED, NT, f32x4>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
-  } else if constexpr (sizeof(T) == 4) {
-    const f32x4 a = load16<NT, f32x4>(p), b = load16<NT, f32x4>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
-    }
+    for (int i = 0; i < 4; ++i) v[i] = a[i];
   } else {
-    const u32x4 a = load16<NT, u32x4>(p);
+    const u32x4 a = load16<ALIGNED, NT, u32x4>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack2<T>(a[i], v[2 * i], v[2 * i + 1]);
   }
 }
 template <typename T, bool ALIGNED, bool NT = false>
-__device__ __forceinline__ void store8(T* p, const float* v) {
-  if constexpr (!ALIGNED) {
+__device__ __forceinline__ void store_vec(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4) store16<ALIGNED, NT>(p, f32x4{v[0], v[1], v[2], v[3]});
+  else
+    store16<ALIGNED, NT>(p, u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])});
+}
+
+// eight consecutive elements
+template <typename T, bool ALIGNED, bool NT = false>
+__device__ __forceinline__ void load8(const T* p, float* v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = from_f32<T>(v[i]);
-  } else if constexpr (sizeof(T) == 4) {
-    store16<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
-    store16<NT>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
-  } else {
-    store16<NT>(p, u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])});
-  }
+  for (int i = 0; i < 8; i += kVec<T>) load_vec<T, ALIGNED, NT>(p + i, v + i);
+}
+template <typename T, bool ALIGNED, bool NT = false>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; i += kVec<T>) store_vec<T, ALIGNED, NT>(p + i, v + i);
 }
 
 // Bytes from which on an operand that is read once is read with the

@@ -17,6 +17,7 @@ forward pass with it on ``x.detach().requires_grad_()``, or call
 
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -56,6 +57,9 @@ class TokenOrder:
         return self.offsets.data_ptr() + 4 * self.num_experts
 
 
+_sort_workspace = lru_cache(maxsize=256)(M.moe_sort_tokens_workspace_bytes)
+
+
 def sort_tokens(ids: torch.Tensor, num_experts: int) -> TokenOrder:
     """The order of the pairs of ``ids`` (int32 or int64 [T, k]) sorted by expert;
     ids outside [0, num_experts) are dropped (-1: padding)."""
@@ -65,7 +69,7 @@ def sort_tokens(ids: torch.Tensor, num_experts: int) -> TokenOrder:
     if not ids.is_contiguous():
         ids = ids.contiguous()
     t, k = ids.shape
-    need = M.moe_sort_tokens_workspace_bytes(t, k, num_experts)
+    need = _sort_workspace(t, k, num_experts)
     device = ids.device
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=device)
     row_src = torch.empty(t * k, dtype=torch.int32, device=device)
