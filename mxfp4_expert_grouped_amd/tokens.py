@@ -161,29 +161,29 @@ def _check_weights(weights: Optional[torch.Tensor], order: TokenOrder) -> None:
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
-        ctx.order = order
+        # saved as tensors, so that a change of the order in place before the backward pass is an error
+        ctx.save_for_backward(order.offsets, order.row_src, order.token_row)
         return _dispatch(x, order)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs):
-        return _combine(dxs, None, ctx.order), None
+        return _combine(dxs, None, TokenOrder(*ctx.saved_tensors)), None
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weights, order):
         need_w = weights is not None and weights.requires_grad
-        ctx.order = order
-        ctx.save_for_backward(rows if need_w else None, weights)
+        ctx.save_for_backward(rows if need_w else None, weights, order.offsets, order.row_src, order.token_row)
         return _combine(rows, weights, order)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        rows, weights = ctx.saved_tensors
+        rows, weights, *order = ctx.saved_tensors
         need_rows, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        return (*combine_backward(dy, rows, weights, ctx.order, need_rows, need_w), None)
+        return (*combine_backward(dy, rows, weights, TokenOrder(*order), need_rows, need_w), None)
 
 
 def dispatch(x: torch.Tensor, order: TokenOrder) -> torch.Tensor:

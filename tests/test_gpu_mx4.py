@@ -305,6 +305,23 @@ def test_linear_nan_scales(L, rows, k, n):
     assert_linear(got.nan_to_num(0.0), np.where(nan, 0, y), mag, k, "fp32")
 
 
+@pytest.mark.parametrize("rows,k,n", [(4, 512, 40), (90, 96, 64), (700, 1024, 4096), (2048, 384, 8192)])
+def test_linear_of_a_row_that_is_not_finite(L, rows, k, n):
+    # what the quantiser makes of an infinity (scale 255, codes 0) poisons the row's results, and no other's
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((rows, k), generator=g, device="cuda")
+    w = torch.randn((n, k), generator=g, device="cuda")
+    wc, ws = L.quantize_mx4(w)
+    c, s = L.quantize_mx4(x)
+    good = L.linear_mx4(c, s, wc, ws)
+    x[2, k - 5] = float("inf")
+    c, s = L.quantize_mx4(x)
+    got = L.linear_mx4(c, s, wc, ws)
+    assert got[2].isnan().all()
+    got[2] = good[2]
+    assert torch.equal(got, good)
+
+
 @pytest.mark.parametrize("rows,k,n", [(2, 512, 20), (40, 512, 256), (300, 512, 256), (2, 128, 20), (600, 512, 8192),
                                       (600, 96, 300)])
 def test_linear_extreme_scales(L, rows, k, n):

@@ -209,6 +209,55 @@ def test_only_the_gradients_that_are_asked_for(K):
     assert K.combine(rows.detach(), w.detach(), order).grad_fn is None
 
 
+def test_an_order_changed_before_the_backward_pass_is_an_error(K):
+    ids, v, _ = case(20, 3, 5, 64, "fp32", "random", seed=81)
+    order = K.sort_tokens(torch.from_numpy(ids).cuda(), 5)
+    x, w = v["x"].requires_grad_(), v["w"].requires_grad_()
+    xs, y = K.dispatch(x, order), K.combine(v["rows"], w, order)
+    order.token_row.zero_()
+    with pytest.raises(RuntimeError, match="inplace"):
+        torch.autograd.grad(xs, x, v["dxs"])
+    with pytest.raises(RuntimeError, match="inplace"):
+        torch.autograd.grad(y, w, v["dy"])
+
+
+def test_a_second_derivative_is_refused(K):
+    ids, v, _ = case(20, 3, 5, 64, "fp32", "random", seed=82)
+    order = K.sort_tokens(torch.from_numpy(ids).cuda(), 5)
+    x, w = v["x"].requires_grad_(), v["w"].requires_grad_()
+    y = K.combine(K.dispatch(x, order), w, order)
+    gx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(gx.sum(), w)
+
+
+def test_two_graphs_replayed_in_turn(K):
+    # each capture has a workspace and buffers of its own (more pairs than one workgroup sorts)
+    sets = []
+    for i in range(2):
+        ids, v, _ = case(1500, 8, 64, 40, "bf16", "dropped", seed=200 + i)
+        ids = torch.from_numpy(ids).cuda()
+
+        def step(ids=ids, v=v):
+            order = K.sort_tokens(ids, 64)
+            return order.row_src, K.combine(K.dispatch(v["x"], order), v["w"], order)
+
+        ref = [o.clone() for o in step()]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        sets.append((graph, out, ref))
+    for _ in range(3):
+        for graph, out, _ in sets:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, ref in sets:
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))
+        for _, out, _ in sets:
+            for o in out:
+                o.zero_()
+
+
 def test_broadcast_and_strided_inputs(K):
     t, k, e, d = 37, 4, 8, 48
     ids, v, r = case(t, k, e, d, "fp32", "dropped", seed=90)
