@@ -246,14 +246,14 @@ def test_two_graphs_replayed_in_turn(K):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             out = step()
-        sets.append((graph, out, ref))
+        sets.append((graph, out, ref, ids, v))  # (a graph reads its inputs: they live as long)
     for _ in range(3):
-        for graph, out, _ in sets:
+        for graph, *_ in sets:
             graph.replay()
         torch.cuda.synchronize()
-        for _, out, ref in sets:
+        for _, out, ref, *_ in sets:
             assert all(torch.equal(a, b) for a, b in zip(out, ref))
-        for _, out, _ in sets:
+        for _, out, *_ in sets:
             for o in out:
                 o.zero_()
 
