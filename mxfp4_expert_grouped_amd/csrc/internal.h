@@ -170,7 +170,7 @@ hipError_t launch_pack_mx4(const uint8_t* codes, const uint8_t* scales, int64_t 
 
 // ---- the standalone pieces: MXFP4 conversion and product, token order
 
-// element types of rows (row_types.h)
+// element types of rows (row_types.h has their arithmetic)
 enum class RowType { kBf16, kFp16, kFp32 };
 
 hipError_t launch_quantize_mx4(const void* src, RowType dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
