@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   };
   // (total and G are at most 2^30: no overflow)
   auto next_pos = [&](int pos) { return pos + G; };
-  // Copy number m of the step at the issue side, the I-th of its pair.
+  // Copy number m of the step at the issue side, the I-th of its group.
   auto issue = [&](auto ic, auto mc) {
     constexpr int I = decltype(ic)::value, m = decltype(mc)::value, n = m - P::CA - P::CW;
     const uint32_t slot = lds0 + iss_slot * P::SLOT;

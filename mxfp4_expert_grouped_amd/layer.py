@@ -158,8 +158,8 @@ def quantize_mx4(src: torch.Tensor):
     if cols and (step != 1 or ld < cols):
         src = src.contiguous()
         ld = cols
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=src.device)
-    scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=src.device)
+    codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=src.device)
+    scales = torch.empty(rows, cols // 32, dtype=torch.uint8, device=src.device)
     on_device(dev, M.moe_quantize_mx4, src.data_ptr(), dt, rows, cols, max(ld, cols), codes.data_ptr(),
               scales.data_ptr())
     return codes, scales
@@ -171,7 +171,7 @@ def dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype
     dev = device_index(codes, scales)
     codes, scales, cols = _mx4_operand(codes, scales, "matrix", 2)
     rows = codes.shape[0]
-    out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    out = torch.empty(rows, cols, dtype=dtype, device=codes.device)
     on_device(dev, M.moe_dequantize_mx4, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dt, cols)
     return out
 
@@ -203,7 +203,7 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
         at = offsets.data_ptr()
     rows = codes.shape[0]
     if out is None:
-        out, ld = torch.empty((rows, n), dtype=dtype, device=codes.device), n
+        out, ld = torch.empty(rows, n, dtype=dtype, device=codes.device), n
     else:
         ld = out.stride(0) if out.dim() == 2 and rows > 1 else n
         if out.shape != (rows, n) or (n and out.stride(1) != 1) or ld < n:

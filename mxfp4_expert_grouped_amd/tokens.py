@@ -73,7 +73,7 @@ def sort_tokens(ids: torch.Tensor, num_experts: int) -> TokenOrder:
     device = ids.device
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=device)
     row_src = torch.empty(t * k, dtype=torch.int32, device=device)
-    token_row = torch.empty((t, k), dtype=torch.int32, device=device)
+    token_row = torch.empty(t, k, dtype=torch.int32, device=device)
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     on_device(dev, M.moe_sort_tokens, ids.data_ptr(),
               M.MOE_ID_INT64 if ids.dtype is torch.int64 else M.MOE_ID_INT32, t, k, num_experts, offsets.data_ptr(),
@@ -100,7 +100,7 @@ def _dispatch(x: torch.Tensor, order: TokenOrder) -> torch.Tensor:
     t, k = tr.shape
     x, ld = _matrix(x, t, "x")
     d = x.shape[1]
-    xs = torch.empty((t * k, d), dtype=x.dtype, device=x.device)
+    xs = torch.empty(t * k, d, dtype=x.dtype, device=x.device)
     sz = x.element_size()
     on_device(dev, M.moe_dispatch_rows, x.data_ptr(), d * sz, ld * sz, tr.data_ptr(), t, k, order._num_rows(), t * k,
               xs.data_ptr(), d * sz)
@@ -115,7 +115,7 @@ def _combine(rows: torch.Tensor, weights: Optional[torch.Tensor], order: TokenOr
     if weights is not None and not weights.is_contiguous():
         weights = weights.contiguous()
     d = rows.shape[1]
-    y = torch.empty((t, d), dtype=rows.dtype, device=rows.device)
+    y = torch.empty(t, d, dtype=rows.dtype, device=rows.device)
     on_device(dev, M.moe_combine_rows, rows.data_ptr(), row_dtype(rows.dtype), t * k, d, ld, tr.data_ptr(),
               weights.data_ptr() if weights is not None else None, t, k, y.data_ptr(), d)
     return y
@@ -145,8 +145,8 @@ def combine_backward(dy: torch.Tensor, rows: Optional[torch.Tensor], weights: Op
         rows, ld_rows = _matrix(rows, t * k, "rows")
     if weights is not None:
         weights = weights.contiguous()
-    drows = torch.empty((t * k, d), dtype=dy.dtype, device=dy.device) if need_rows else None
-    dw = torch.empty((t, k), dtype=torch.float32, device=dy.device) if need_weights else None
+    drows = torch.empty(t * k, d, dtype=dy.dtype, device=dy.device) if need_rows else None
+    dw = torch.empty(t, k, dtype=torch.float32, device=dy.device) if need_weights else None
     ptr = lambda x: x.data_ptr() if x is not None else None  # noqa: E731
     on_device(dev, M.moe_combine_rows_backward, dy.data_ptr(), ptr(rows), dt, t * k, d, ld_dy, ld_rows,
               order.token_row.data_ptr(), ptr(weights), t, k, order._num_rows(), ptr(drows), d, ptr(dw))
