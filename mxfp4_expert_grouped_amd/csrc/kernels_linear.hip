@@ -646,10 +646,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     if (I == U - 1) group ^= 1;
   };
 
-  // ---- results: acc[i][j] of this wave.  Buffer stores with the tile's first
-  // row as base: a lane whose row or columns are not there takes an offset past
-  // the buffer's end and stores nothing, so there are no branches (which would
-  // cost copies of the accumulators).
+  // ---- results: acc[i][j] of this wave.  WIDE: buffer stores with the tile's
+  // first row as base: a lane whose row or columns are not there takes an
+  // offset past the buffer's end and stores nothing, so there are no branches
+  // (which would cost copies of the accumulators).  Otherwise the same 16-byte
+  // pieces at any address, and only a row's last one by elements (8192 x 4095,
+  // k = 2048, bf16: 66 us, 121 us with every element on its own; 4096 columns
+  // 40 us, all of it whole cache lines).
   constexpr uint32_t kNowhere = 0x80000000u;  // the buffer ends here
   auto store_tile = [&](const TileAt& t) {
     constexpr int SZ = sizeof(T), PER = 16 / SZ;
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     // this lane's rows: with 16-bit results lane l stores rows l%16 and
     // 16 + l%16 of each block of 32, otherwise row l%32
-    constexpr bool HALVES = WIDE && SZ == 2;
+    constexpr bool HALVES = SZ == 2;
     constexpr int NR = HALVES ? 2 : 1;
     uint32_t at[MI][NR];
 #pragma unroll
@@ -686,7 +689,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
         return f;
       };
       auto put = [&](int h, int cx, v4u v) {
-        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, cx < cols ? at[i][h] + cx * SZ : kNowhere, 0, 0);
+        if constexpr (WIDE) {
+          __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, cx < cols ? at[i][h] + cx * SZ : kNowhere, 0, 0);
+        } else if (at[i][h] != kNowhere && cx < cols) {
+          // rows anywhere in memory, and a row's last piece in part
+          char* to = reinterpret_cast<char*>(base) + at[i][h] + cx * SZ;
+          if (cx + PER <= cols) {
+            store16<false, false>(to, v);
+          } else {
+#pragma unroll
+            for (int x = 0; x < PER - 1; ++x) {
+              if (cx + x >= cols) break;
+              if constexpr (SZ == 2) reinterpret_cast<uint16_t*>(to)[x] = static_cast<uint16_t>(v[x / 2] >> (16 * (x % 2)));
+              else reinterpret_cast<uint32_t*>(to)[x] = v[x];
+            }
+          }
+        }
       };
       const int col = (wn * NI + j) * 32;
       if constexpr (HALVES) {
@@ -717,19 +735,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if constexpr (WIDE) {
-            const v4f v = {c(4 * q), c(4 * q + 1), c(4 * q + 2), c(4 * q + 3)};
-            put(0, col + 8 * q + 4 * g32, __builtin_bit_cast(v4u, v));
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int cx = col + 8 * q + 4 * g32 + x;
-              const uint32_t off = cx < cols ? at[i][0] + cx * SZ : kNowhere;
-              const T v = from_f32<T>(c(4 * q + x));
-              if constexpr (SZ == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), rsrc, off, 0, 0);
-              else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, off, 0, 0);
-            }
-          }
+          const v4f v = {c(4 * q), c(4 * q + 1), c(4 * q + 2), c(4 * q + 3)};
+          put(0, col + 8 * q + 4 * g32, __builtin_bit_cast(v4u, v));
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   bool stored = false;
   for (int pos = first; pos < total; pos = next_pos(pos)) {
     const TileAt t = tile_at(pos);
-    // a store that did not go by 16-byte pieces is not counted: wait for it
+    // without WIDE the number of stores is not known here: wait for all
     if (!WIDE && stored) wait_vm<0>();
     stored &= WIDE;
     if constexpr (GS) {
@@ -827,8 +834,10 @@ template <typename T, int BM>
 hipError_t tile_t(const LinearArgs& a, hipStream_t st) {
   const int64_t sb = a.k / 32;
   const bool wide = rows_aligned(a.y, a.ld_y * sizeof(T), 16) && a.n % (16 / sizeof(T)) == 0;
-  // (single-element stores and 256 rows need more registers than there are)
-  if constexpr (BM == 256)
+  // (256 rows of fp32 and partial pieces need more registers than there are;
+  // with 16-bit results they fit: 8192 x 4095, k = 7168, 160 us against 197 us
+  // in tiles of 128 rows)
+  if constexpr (BM == 256 && sizeof(T) == 4)
     if (!wide) return tile_t<T, 128>(a, st);
   const bool pieces = a.k % 512 == 0 && rows_aligned(a.a_s, sb, 16) && rows_aligned(a.w_s, sb, 16);
   const bool once = a.rows <= (a.offsets ? 32 * a.mats : 64);
@@ -838,7 +847,7 @@ hipError_t tile_t(const LinearArgs& a, hipStream_t st) {
     k<<<grid, kTileThreads, 0, st>>>(a);
     return hipGetLastError();
   };
-  if constexpr (BM != 256)
+  if constexpr (BM != 256 || sizeof(T) != 4)
     if (!wide) return go(k_linear_tile<T, BM, 0, false, false>);
   if constexpr (BM == 64) {
     if (pieces && a.k % 1024 == 0)

@@ -271,6 +271,27 @@ def test_linear_leaves_rows_outside_the_offsets(L, k, n, per):
     assert (whole == 7.25).all()
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,gap", [(4089, 0), (4090, 3), (4091, 1), (4092, 0), (4093, 5), (4094, 1), (4095, 8), (4096, 1)])
+def test_linear_rows_of_y_anywhere(L, n, gap, dtype):
+    # every number of columns in a row's last piece, rows that begin anywhere, in tiles of many rows: what lies
+    # between the rows, before the first and behind the last, stays as it was
+    k, offsets = 256, [0, 1200, 1200, 1777, 2048]
+    ac, asc = random_mx4((2048,), k, 900 + n)
+    wc, wsc = random_mx4((4, n), k, 1000 + n)
+    if dtype == "fp16":
+        asc -= 6
+    y, mag = linear_ref(ac, asc, wc, wsc, offsets)
+    ld, lead = n + gap, 1
+    flat = torch.full((lead + 2048 * ld + 64,), 7.0, dtype=DT[dtype], device="cuda")
+    out = flat[lead:lead + 2048 * ld].view(2048, ld)[:, :n]
+    c = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    L.linear_mx4(c(ac), c(asc), c(wc), c(wsc), offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=out)
+    assert_linear(out, y, mag, k, dtype)
+    assert bool((flat[:lead] == 7).all()) and bool((flat[lead + 2048 * ld:] == 7).all())
+    assert bool((flat[lead:lead + 2048 * ld].view(2048, ld)[:, n:] == 7).all())
+
+
 @pytest.mark.parametrize("rows,k", [(4, 512), (100, 512), (4, 96), (600, 1024), (3000, 640)])
 def test_linear_offsets_out_of_range_stay_inside(L, rows, k):
     n = 40 if rows < 3000 else 2000
