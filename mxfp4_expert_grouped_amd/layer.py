@@ -7,6 +7,7 @@ from dataclasses import dataclass
 from typing import Dict, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import mxmoe as M
 
@@ -106,7 +107,13 @@ def row_dtype(dtype: torch.dtype) -> int:
 
 
 def device_index(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
-    """The GPU that every tensor is on (a call's launches go to its current stream)."""
+    """The GPU that every tensor is on (a call's launches go to its current stream).
+    A tensor with a forward-mode tangent is refused: the kernels see values only,
+    and their outputs would come without one."""
+    if forward_ad._current_level >= 0:  # (inside a dual_level: elsewhere there are no tangents)
+        for t in (first, *others):
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("a tensor has a forward-mode tangent, and there is no forward-mode derivative here")
     if not first.is_cuda:
         raise ValueError(f"expected tensors on a GPU, got one on {first.device}")
     index = first.get_device()

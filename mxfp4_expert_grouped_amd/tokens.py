@@ -6,7 +6,8 @@ moe_dispatch_rows, moe_combine_rows and moe_combine_rows_backward).
     rows = ...                                     # expert e has rows offsets[e] .. offsets[e+1]-1
     y = combine(rows, weights, order)              # [T, d]
 
-``dispatch`` and ``combine`` are differentiable (x; rows and weights), once.
+``dispatch`` and ``combine`` are differentiable (x; rows and weights), once and
+backwards: tensors with a forward-mode tangent are refused.
 Every call goes to the current stream of its tensors' GPU; nothing is
 synchronised, so all of it can be captured into a graph.  A backward pass that
 is captured needs leaves that no graph built outside the capture still holds
