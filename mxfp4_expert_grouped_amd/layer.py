@@ -8,6 +8,7 @@ from typing import Dict, Optional
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import mxmoe as M
 
@@ -192,8 +193,11 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
     with a leading axis of matrices [E, N, ...] and ``offsets`` int32 [E+1]:
     rows offsets[e] .. offsets[e+1]-1 take matrix e.  Rows outside every range
     are left as they were in ``out``; without ``out`` they are undefined.
-    No gradient: the product is for inference.
+    No gradient: the product is for inference, and ``out`` may not require one
+    (except under no_grad).
     """
+    if out is not None and out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out requires a gradient, and the product has none")
     grouped = offsets is not None
     dev = device_index(codes, scales, w_codes, w_scales, offsets, out)
     codes, scales, k = _mx4_operand(codes, scales, "rows", 2)
@@ -209,7 +213,8 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
             offsets = offsets.contiguous()
         at = offsets.data_ptr()
     rows = codes.shape[0]
-    if out is None:
+    given = out is not None
+    if not given:
         out, ld = torch.empty(rows, n, dtype=dtype, device=codes.device), n
     else:
         ld = out.stride(0) if out.dim() == 2 and rows > 1 else n
@@ -217,4 +222,7 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
             raise ValueError(f"out must be [{rows}, {n}] with dense rows")
     on_device(dev, M.moe_linear_mx4, codes.data_ptr(), scales.data_ptr(), rows, w_codes.data_ptr(),
               w_scales.data_ptr(), mats, at, n, k, out.data_ptr(), row_dtype(out.dtype), ld)
+    if given:
+        # autograd learns of the write: what it saved of out before is no longer there
+        increment_version(out)
     return out

@@ -1,0 +1,67 @@
+"""The layer's pieces beside torch's own operators on the GPU: what autograd,
+views and lazy bits of a tensor ask of a call that goes by addresses."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mxfp4_expert_grouped_amd import mxmoe
+    mxmoe.load_library()
+    torch.cuda.set_device(0)
+    yield
+
+
+@pytest.fixture(scope="module")
+def L():
+    from mxfp4_expert_grouped_amd import layer
+    return layer
+
+
+@pytest.fixture(scope="module")
+def K():
+    from mxfp4_expert_grouped_amd import tokens
+    return tokens
+
+
+def operands(L, rows, n, k, seed):
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g).cuda()  # noqa: E731
+    return (*L.quantize_mx4(rnd(rows, k)), *L.quantize_mx4(rnd(n, k)))
+
+
+def test_a_write_to_out_is_seen_by_autograd(L):
+    # what another operation saved of the buffer before the product is gone: its gradient is an error, not wrong
+    args = operands(L, 5, 8, 64, 1)
+    buf = torch.ones(5, 16, device="cuda")
+    x = torch.ones(5, 8, device="cuda", requires_grad=True)
+    y = x * buf[:, :8]
+    version = buf._version
+    out = L.linear_mx4(*args, out=buf[:, :8])
+    assert buf._version > version and out._version == buf._version
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    # saved after the product it stays, and other calls of the same operands leave it
+    y = x * buf[:, :8]
+    assert torch.equal(L.linear_mx4(*args, dtype=torch.float32), out)
+    y.sum().backward()
+    assert torch.equal(x.grad, out)
+    # a parameter's values under no_grad, as any operator writes them
+    p = torch.nn.Parameter(torch.zeros(5, 8, device="cuda"))
+    with torch.no_grad():
+        L.linear_mx4(*args, out=p)
+    assert torch.equal(p.detach(), out)
+
+
+def test_a_write_to_an_inference_tensor(L):
+    args = operands(L, 5, 8, 64, 2)
+    with torch.inference_mode():
+        out = torch.zeros(5, 8, device="cuda")
+        L.linear_mx4(*args, out=out)
+    assert torch.equal(out.clone(), L.linear_mx4(*args, dtype=torch.float32))

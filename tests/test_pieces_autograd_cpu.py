@@ -37,3 +37,14 @@ def test_a_forward_mode_tangent_is_refused(call):
             TANGENT_CALLS[call](dual, order(4, 2, 3))
         with pytest.raises(ValueError, match="GPU"):  # tensors without one go on to the other checks
             TANGENT_CALLS[call](lambda *s: torch.ones(s), order(4, 2, 3))
+
+
+def test_an_out_that_requires_a_gradient_is_refused():
+    z = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    args = (z(4, 32), z(4, 2), z(8, 32), z(8, 2))
+    leaf = torch.zeros(4, 8, requires_grad=True)
+    for out in (leaf, leaf * 2, leaf[:]):
+        with pytest.raises(ValueError, match="gradient"):
+            L.linear_mx4(*args, out=out)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):  # as for any write into it: on to the other checks
+            L.linear_mx4(*args, out=out)
