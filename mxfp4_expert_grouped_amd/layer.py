@@ -185,7 +185,7 @@ def dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype
 
 
 def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
-               offsets: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+               offsets: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rows times weights, both MXFP4 in canonical form, fp32 accumulation (moe_linear_mx4).
 
@@ -193,11 +193,14 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
     with a leading axis of matrices [E, N, ...] and ``offsets`` int32 [E+1]:
     rows offsets[e] .. offsets[e+1]-1 take matrix e.  Rows outside every range
     are left as they were in ``out``; without ``out`` they are undefined.
+    ``dtype`` is the result's: ``out``'s, or bfloat16 where neither is given.
     No gradient: the product is for inference, and ``out`` may not require one
     (except under no_grad).
     """
     if out is not None and out.requires_grad and torch.is_grad_enabled():
         raise ValueError("out requires a gradient, and the product has none")
+    if out is not None and dtype is not None and dtype != out.dtype:
+        raise ValueError(f"the result is to be {dtype}, and out is {out.dtype}")
     grouped = offsets is not None
     dev = device_index(codes, scales, w_codes, w_scales, offsets, out)
     codes, scales, k = _mx4_operand(codes, scales, "rows", 2)
@@ -215,7 +218,7 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
     rows = codes.shape[0]
     given = out is not None
     if not given:
-        out, ld = torch.empty(rows, n, dtype=dtype, device=codes.device), n
+        out, ld = torch.empty(rows, n, dtype=dtype or torch.bfloat16, device=codes.device), n
     else:
         ld = out.stride(0) if out.dim() == 2 and rows > 1 else n
         if out.shape != (rows, n) or (n and out.stride(1) != 1) or ld < n:
