@@ -221,7 +221,7 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
         out, ld = torch.empty(rows, n, dtype=dtype or torch.bfloat16, device=codes.device), n
     else:
         ld = out.stride(0) if out.dim() == 2 and rows > 1 else n
-        if out.shape != (rows, n) or (n and out.stride(1) != 1) or ld < n:
+        if out.shape != (rows, n) or (n > 1 and out.stride(1) != 1) or ld < n:
             raise ValueError(f"out must be [{rows}, {n}] with dense rows")
     on_device(dev, M.moe_linear_mx4, codes.data_ptr(), scales.data_ptr(), rows, w_codes.data_ptr(),
               w_scales.data_ptr(), mats, at, n, k, out.data_ptr(), row_dtype(out.dtype), ld)

@@ -65,3 +65,17 @@ def test_a_write_to_an_inference_tensor(L):
         out = torch.zeros(5, 8, device="cuda")
         L.linear_mx4(*args, out=out)
     assert torch.equal(out.clone(), L.linear_mx4(*args, dtype=torch.float32))
+
+
+def test_an_out_of_one_column(L):
+    # the stride along a single column says nothing: a transposed row, a column of a matrix
+    args = operands(L, 6, 1, 64, 3)
+    ref = L.linear_mx4(*args, dtype=torch.float32)
+    out = torch.zeros(1, 6, device="cuda").t()
+    assert out.stride() == (1, 6)
+    assert torch.equal(L.linear_mx4(*args, out=out), ref)
+    wide = torch.zeros(6, 5, device="cuda")
+    L.linear_mx4(*args, out=wide.as_strided((6, 1), (5, 3), 2))
+    assert torch.equal(wide[:, 2:3], ref) and not wide[:, [0, 1, 3, 4]].any()
+    with pytest.raises(ValueError, match="dense rows"):
+        L.linear_mx4(*args, out=torch.zeros(1, 1, device="cuda").expand(6, 1))
