@@ -271,6 +271,9 @@ moe_status moe_router_bias_update(const moe_plan_t *plan, const int32_t *expert_
  *   rows, or of their codes and scales -> moe_linear_mx4 with the order's
  *   offsets -> the caller's activation -> moe_quantize_mx4 -> moe_linear_mx4
  *   -> moe_combine_rows.
+ * Gradients there are of dispatch (moe_combine_rows without weights) and of
+ * combine (moe_combine_rows_backward); none of the MXFP4 conversions and of
+ * their product.
  * Errors and streams as for moe_forward.  What device memory holds (ids, row
  * numbers, offsets) cannot be checked on the host: values outside their range
  * are treated as said at each call and never reach outside a buffer. */

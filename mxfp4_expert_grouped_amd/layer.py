@@ -154,7 +154,10 @@ def _mx4_operand(codes: torch.Tensor, scales: torch.Tensor, what: str, dims: int
 def quantize_mx4(src: torch.Tensor):
     """MXFP4 codes (uint8 [rows, cols/2]) and scales (uint8 [rows, cols/32]) of a
     2-D bf16, fp16 or fp32 tensor along its last axis, in the canonical form of
-    the expert weights (moe_quantize_mx4)."""
+    the expert weights (moe_quantize_mx4).  Codes carry no gradient: a source
+    that requires one is refused (``detach`` it, or call under no_grad)."""
+    if src.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the source requires a gradient, and MXFP4 codes have none: detach it")
     if src.dim() != 2:
         raise ValueError(f"expected a matrix, got {src.dim()} dimensions")
     dt = row_dtype(src.dtype)

@@ -48,3 +48,14 @@ def test_an_out_that_requires_a_gradient_is_refused():
             L.linear_mx4(*args, out=out)
         with torch.no_grad(), pytest.raises(ValueError, match="GPU"):  # as for any write into it: on to the other checks
             L.linear_mx4(*args, out=out)
+
+
+def test_quantising_what_requires_a_gradient_is_refused():
+    # the codes could not pass it on: a chain through them would train without a word
+    leaf = torch.zeros(4, 32, requires_grad=True)
+    for src in (leaf, leaf * 2):
+        with pytest.raises(ValueError, match="gradient"):
+            L.quantize_mx4(src)
+        for call in (lambda: L.quantize_mx4(src.detach()), torch.no_grad()(lambda: L.quantize_mx4(src))):
+            with pytest.raises(ValueError, match="GPU"):  # on to the other checks
+                call()
