@@ -124,6 +124,12 @@ def device_index(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     return index
 
 
+def in_memory(t: torch.Tensor) -> torch.Tensor:
+    """t, with its values where its address says: a conjugated view, or its
+    imaginary part, shares the memory of the values before."""
+    return t.resolve_conj().resolve_neg() if t.is_neg() or t.is_conj() else t
+
+
 def on_device(index: int, call, *args) -> None:
     """call(*args, stream) with GPU ``index`` current and its current stream.  A few
     small calls are bound by the host: the device is switched only if it has to be."""
@@ -165,6 +171,7 @@ def quantize_mx4(src: torch.Tensor):
     rows, cols = src.shape
     if cols % 32:
         raise ValueError(f"columns ({cols}) must be a multiple of 32")
+    src = in_memory(src)
     ld, step = src.stride()
     if cols and (step != 1 or ld < cols):
         src = src.contiguous()
@@ -223,6 +230,8 @@ def linear_mx4(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
     if not given:
         out, ld = torch.empty(rows, n, dtype=dtype or torch.bfloat16, device=codes.device), n
     else:
+        if out.is_neg():
+            raise ValueError("out is a lazily negated view")
         ld = out.stride(0) if out.dim() == 2 and rows > 1 else n
         if out.shape != (rows, n) or (n > 1 and out.stride(1) != 1) or ld < n:
             raise ValueError(f"out must be [{rows}, {n}] with dense rows")

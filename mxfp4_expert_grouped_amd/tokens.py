@@ -25,7 +25,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import mxmoe as M
-from .layer import device_index, on_device, row_dtype
+from .layer import device_index, in_memory, on_device, row_dtype
 
 
 class TokenOrder:
@@ -87,6 +87,7 @@ def _matrix(x: torch.Tensor, rows: int, what: str):
     if x.dim() != 2 or x.shape[0] != rows:
         raise ValueError(f"{what} must be [{rows}, d], got {tuple(x.shape)}")
     d = x.shape[1]
+    x = in_memory(x)
     ld, step = x.stride()
     if d == 0 or rows == 0:
         return x, d
@@ -113,8 +114,8 @@ def _combine(rows: torch.Tensor, weights: Optional[torch.Tensor], order: TokenOr
     tr = order.token_row
     t, k = tr.shape
     rows, ld = _matrix(rows, t * k, "rows")
-    if weights is not None and not weights.is_contiguous():
-        weights = weights.contiguous()
+    if weights is not None:
+        weights = in_memory(weights).contiguous()
     d = rows.shape[1]
     y = torch.empty(t, d, dtype=rows.dtype, device=rows.device)
     on_device(dev, M.moe_combine_rows, rows.data_ptr(), row_dtype(rows.dtype), t * k, d, ld, tr.data_ptr(),
@@ -145,7 +146,7 @@ def combine_backward(dy: torch.Tensor, rows: Optional[torch.Tensor], weights: Op
     if rows is not None:
         rows, ld_rows = _matrix(rows, t * k, "rows")
     if weights is not None:
-        weights = weights.contiguous()
+        weights = in_memory(weights).contiguous()
     drows = torch.empty(t * k, d, dtype=dy.dtype, device=dy.device) if need_rows else None
     dw = torch.empty(t, k, dtype=torch.float32, device=dy.device) if need_weights else None
     ptr = lambda x: x.data_ptr() if x is not None else None  # noqa: E731

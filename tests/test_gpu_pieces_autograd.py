@@ -79,3 +79,43 @@ def test_an_out_of_one_column(L):
     assert torch.equal(wide[:, 2:3], ref) and not wide[:, [0, 1, 3, 4]].any()
     with pytest.raises(ValueError, match="dense rows"):
         L.linear_mx4(*args, out=torch.zeros(1, 1, device="cuda").expand(6, 1))
+
+
+def lazy(shape, seed):
+    """a float32 tensor of which memory holds the negative (the imaginary part of a conjugate), and its values"""
+    g = torch.Generator().manual_seed(seed)
+    z = torch.complex(torch.randn(shape, generator=g), torch.randn(shape, generator=g)).cuda()
+    t = z.conj().imag
+    assert t.is_neg()
+    return t, -z.imag
+
+
+@pytest.mark.parametrize("t,d", [(5, 64), (7, 1), (1, 96)])
+def test_values_that_memory_does_not_hold(L, K, t, d):
+    k, e = 2, 4
+    order = K.sort_tokens(torch.randint(0, e, (t, k), generator=torch.Generator().manual_seed(4)).cuda(), e)
+    x, xv = lazy((t, d), 5)
+    rows, rv = lazy((t * k, d), 6)
+    w, wv = lazy((t, k), 7)
+    assert torch.equal(K.dispatch(x, order), K.dispatch(xv, order))
+    assert torch.equal(K.dispatch_backward(rows, order), K.dispatch_backward(rv, order))
+    assert torch.equal(K.combine(rows, w, order), K.combine(rv, wv, order))
+    for got, ref in zip(K.combine_backward(x, rows, w, order), K.combine_backward(xv, rv, wv, order)):
+        assert torch.equal(got, ref)
+    a, b = rows.detach().requires_grad_(), rv.clone().requires_grad_()
+    u, v = w.detach().requires_grad_(), wv.clone().requires_grad_()
+    for got, ref in zip(torch.autograd.grad(K.combine(a, u, order), (a, u), x), torch.autograd.grad(K.combine(b, v, order), (b, v), xv)):
+        assert torch.equal(got, ref)
+    # complex elements move as any others do
+    z = torch.randn(t, d, dtype=torch.complex64, device="cuda")
+    assert torch.equal(K.dispatch(z.conj(), order), K.dispatch(z.conj().resolve_conj(), order))
+    if d % 32 == 0:
+        for got, ref in zip(L.quantize_mx4(x), L.quantize_mx4(xv)):
+            assert torch.equal(got, ref)
+
+
+def test_an_out_that_memory_does_not_hold_is_refused(L):
+    args = operands(L, 4, 8, 64, 8)
+    out, _ = lazy((4, 8), 9)
+    with pytest.raises(ValueError, match="negated"):
+        L.linear_mx4(*args, out=out)
