@@ -29,13 +29,26 @@ from .layer import device_index, in_memory, on_device, row_dtype
 
 
 class TokenOrder:
-    """Which row belongs to which (token, choice): see moe_sort_tokens."""
+    """Which row belongs to which (token, choice): see moe_sort_tokens.  Fixed once
+    it is made; the calls go by its tensors' addresses, so these are checked here."""
     __slots__ = ("offsets", "row_src", "token_row")
 
     def __init__(self, offsets: torch.Tensor, row_src: torch.Tensor, token_row: torch.Tensor):
-        self.offsets = offsets      # int32 [E+1] first row of each expert; offsets[E] rows in all
-        self.row_src = row_src      # int32 [T*k] pair t*k + j of each row, -1 behind the last
-        self.token_row = token_row  # int32 [T, k] row of each pair, -1 for a dropped one
+        for name, t, dims in (("offsets", offsets, 1), ("row_src", row_src, 1), ("token_row", token_row, 2)):
+            if t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimensions")
+            if t.device != token_row.device:
+                raise ValueError(f"tensors on different devices: {t.device} and {token_row.device}")
+        if offsets.numel() < 2 or row_src.numel() != token_row.numel():
+            raise ValueError(f"offsets {list(offsets.shape)}, row_src {list(row_src.shape)} and token_row "
+                             f"{list(token_row.shape)} are not [E+1], [T*k] and [T, k]")
+        _fill(self, offsets, row_src, token_row)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a TokenOrder does not change: make another one")
+
+    def __reduce__(self):
+        return TokenOrder, (self.offsets, self.row_src, self.token_row)
 
     @property
     def num_experts(self) -> int:
@@ -56,6 +69,22 @@ class TokenOrder:
 
     def _num_rows(self) -> int:
         return self.offsets.data_ptr() + 4 * self.num_experts
+
+
+# (the slots' own setters: __setattr__ refuses)
+_set_offsets, _set_row_src, _set_token_row = (TokenOrder.__dict__[n].__set__ for n in TokenOrder.__slots__)
+
+
+def _fill(order: TokenOrder, offsets: torch.Tensor, row_src: torch.Tensor, token_row: torch.Tensor) -> TokenOrder:
+    _set_offsets(order, offsets)      # int32 [E+1] first row of each expert; offsets[E] rows in all
+    _set_row_src(order, row_src)      # int32 [T*k] pair t*k + j of each row, -1 behind the last
+    _set_token_row(order, token_row)  # int32 [T, k] row of each pair, -1 for a dropped one
+    return order
+
+
+def _own_order(*tensors: torch.Tensor) -> TokenOrder:
+    """An order of tensors made here (the checks take a tenth of a small call)."""
+    return _fill(object.__new__(TokenOrder), *tensors)
 
 
 _sort_workspace = lru_cache(maxsize=256)(M.moe_sort_tokens_workspace_bytes)
@@ -79,7 +108,7 @@ def sort_tokens(ids: torch.Tensor, num_experts: int) -> TokenOrder:
     on_device(dev, M.moe_sort_tokens, ids.data_ptr(),
               M.MOE_ID_INT64 if ids.dtype is torch.int64 else M.MOE_ID_INT32, t, k, num_experts, offsets.data_ptr(),
               row_src.data_ptr(), token_row.data_ptr(), ws.data_ptr() if need else None, need)
-    return TokenOrder(offsets, row_src, token_row)
+    return _own_order(offsets, row_src, token_row)
 
 
 def _matrix(x: torch.Tensor, rows: int, what: str):
@@ -170,7 +199,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs):
-        return _combine(dxs, None, TokenOrder(*ctx.saved_tensors)), None
+        return _combine(dxs, None, _own_order(*ctx.saved_tensors)), None
 
 
 class _Combine(torch.autograd.Function):
@@ -185,7 +214,7 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, dy):
         rows, weights, *order = ctx.saved_tensors
         need_rows, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        return (*combine_backward(dy, rows, weights, TokenOrder(*order), need_rows, need_w), None)
+        return (*combine_backward(dy, rows, weights, _own_order(*order), need_rows, need_w), None)
 
 
 def dispatch(x: torch.Tensor, order: TokenOrder) -> torch.Tensor:
