@@ -309,10 +309,14 @@ moe_status moe_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, int64
  * expert_offsets tap); rows before the first and from the last offset on are
  * neither read nor written.  Offsets outside [0, rows] are taken as the
  * nearer end; a matrix whose end lies before its start has no rows; ranges
- * that overlap give undefined values in the rows that they share.
+ * that overlap give undefined values in the rows that they share (and those
+ * that hold more than 2^30 of the tiles below between them may leave rows as
+ * they were).
  * A block with scale 255 makes the sums it enters NaN.
  * 0 <= rows <= 2^25 and 0 <= n (0: nothing is enqueued); 1 <= mats <= 1024;
- * k a multiple of 32 in 32 .. 65536, n <= 2^20, else MOE_ERR_UNSUPPORTED.
+ * k a multiple of 32 in 32 .. 65536, n <= 2^20 and at most 2^30 tiles of 64
+ * rows x 256 columns, (ceil(rows/64) + mats) * ceil(n/256), else
+ * MOE_ERR_UNSUPPORTED.
  * a_codes and w_codes 16-byte, offsets 4-byte aligned, y aligned to its
  * element.  k a multiple of 512 (then 128) is the fast case. */
 moe_status moe_linear_mx4(const uint8_t *a_codes, const uint8_t *a_scales, int64_t rows,

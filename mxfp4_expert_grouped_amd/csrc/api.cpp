@@ -726,6 +726,8 @@ moe_status moe_linear_mx4(const uint8_t* a_codes, const uint8_t* a_scales, int64
   if (k % 32 || k > 65536) return fail(MOE_ERR_UNSUPPORTED, "k (%lld) must be a multiple of 32, at most 65536", static_cast<long long>(k));
   if (mats > 1024 || n > (1 << 20) || rows > (1 << 25))
     return fail(MOE_ERR_UNSUPPORTED, "more than 1024 matrices, 2^20 columns or 2^25 rows");
+  if (linear_tiles_max(rows, mats, n) > kMaxLinearTiles)
+    return fail(MOE_ERR_UNSUPPORTED, "more than 2^30 tiles of 64 rows x 256 columns");
   if (ld_y < n) return fail(MOE_ERR_INVALID_ARG, "ld_y < n");
   if (ld_y > (int64_t(1) << 32)) return fail(MOE_ERR_UNSUPPORTED, "ld_y above 2^32");
   if (rows == 0 || n == 0) return MOE_OK;

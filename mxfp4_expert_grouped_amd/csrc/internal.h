@@ -190,6 +190,10 @@ struct LinearArgs {
   int num_cus;
 };
 hipError_t launch_linear_mx4(const LinearArgs& a, RowType dt, hipStream_t st);
+// Output tiles that a launch counts to, and how many a product may have: in
+// tiles of 64 rows (the lowest) x 256 columns, one more per matrix for its end.
+constexpr int64_t kMaxLinearTiles = int64_t(1) << 30;
+inline int64_t linear_tiles_max(int64_t rows, int64_t mats, int64_t n) { return ((rows + 63) / 64 + mats) * ((n + 255) / 256); }
 
 // pairs sorted by one workgroup in one launch
 constexpr int kSortSmallPairs = 4096;

@@ -368,7 +368,6 @@ __device__ __forceinline__ v16f mfma32_fp4(uint4 w, uint4 a, v16f c, uint32_t sw
 }
 
 constexpr int kTileN = 256, kTileThreads = 256;
-constexpr int kMaxTiles = 1 << 30;
 constexpr int kPanel = 4;  // row tiles that share a column block's weights in time
 
 template <int SZ, int BM, int GS>
@@ -411,9 +410,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   const int mtiles =
       __builtin_amdgcn_readfirstlane(tile_prefix<kTileThreads, BM>(a, prefix, reinterpret_cast<int*>(lds)));
   const int ntn = (a.n + kTileN - 1) / kTileN;
-  // (rows / BM + mats row tiles of at most 4096 column blocks stay below the
-  // limit; only ranges that overlap could have more)
-  const int total = min(mtiles, kMaxTiles / ntn) * ntn;
+  // (the caller has seen to it that rows / BM + mats row tiles stay below the
+  // limit: only ranges that overlap, many times over, can have more)
+  const int total = min(mtiles, static_cast<int>(kMaxLinearTiles) / ntn) * ntn;
   const int nsteps = (a.k + 255) / 256;
   const bool odd = !GS && (a.k & 128);  // the last step is half a step
 

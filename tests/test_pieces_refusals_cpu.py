@@ -49,3 +49,20 @@ def test_an_order_does_not_change():
     for again in (copy.copy(order), copy.deepcopy(order), pickle.loads(pickle.dumps(order))):
         assert all(torch.equal(getattr(again, n), getattr(order, n)) for n in K.TokenOrder.__slots__)
     assert K.TokenOrder(ints(5), ints(0), ints(0, 2)).capacity == 0
+
+
+def test_a_product_of_more_tiles_than_a_launch_counts_is_refused():
+    # (its y would be larger than any memory; the tiles past the limit would have been left out)
+    from mxfp4_expert_grouped_amd import mxmoe as M
+    fake = 1 << 20  # never dereferenced: there is no such device, or the call fails its checks
+
+    def status(rows, mats, n):
+        with pytest.raises(M.MoeError) as ei:
+            M.moe_linear_mx4(fake, fake, rows, fake, fake, mats, fake, n, 128, fake, M.MOE_SRC_BF16, n)
+        return ei.value.status
+
+    for rows, mats, n in ((1 << 25, 1, 1 << 20), (1 << 24, 1, 1 << 20), (1 << 25, 1024, 1 << 19), (64 * ((1 << 18) - 1), 2, 1 << 20)):
+        assert status(rows, mats, n) == M.MOE_ERR_UNSUPPORTED
+    if not torch.cuda.is_available():
+        for rows, mats, n in ((64 * ((1 << 18) - 1), 1, 1 << 20), (1 << 25, 64, 1 << 18)):
+            assert status(rows, mats, n) == M.MOE_ERR_DEVICE
