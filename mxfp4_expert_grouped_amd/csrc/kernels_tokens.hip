@@ -394,8 +394,10 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_rows(const T* __restric
 
 // ---------------------------------------------------------------------------
 // Gradients of combine: a wave per pair reads its row and the token's dy once,
-// drows = w dy (rounded once) and dw = <dy, row> in fp32, lane sums joined by
-// a butterfly (a fixed order).  Bound by memory: 65520 x 7168 fp32 754 us (5.1
+// drows = w dy (rounded once) and dw = <dy, row> in fp32: a lane has a sum for
+// each element of its 16-byte piece, joined in pairs, and the lanes' are joined
+// by a butterfly (a fixed order; of 7168 fp32 columns a product passes through
+// 36 roundings, with one sum per lane it was 118).  Bound by memory: 65520 x 7168 fp32 754 us (5.1
 // TB/s; 925 with the non-temporal hint, as a token's waves share its dy).  A
 // dropped pair has dw = 0.  num_rows (may be
 // null): the wave of pair p also zero-fills the rows p, p + T*k, ... of drows
@@ -419,7 +421,9 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_bwd(const T* __restrict
     const T* row = rows + r * ld;
     T* out = drows ? drows + r * ld_d : nullptr;
     const float f = w ? w[p] : 1.0f;
-    float sum = 0.0f;
+    float sum[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
 #pragma unroll 4
     for (int64_t c = lane; c < pieces; c += 64) {
       float g[VEC];
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_bwd(const T* __restrict
         float v[VEC];
         load_piece<T, FULL>(row, c * VEC, d, v);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sum = fmaf(g[i], v[i], sum);
+        for (int i = 0; i < VEC; ++i) sum[i] = fmaf(g[i], v[i], sum[i]);
       }
       if (out) {
 #pragma unroll
@@ -438,8 +442,12 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_bwd(const T* __restrict
     }
     if (dw) {
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-      if (lane == 0) dw[p] = sum;
+      for (int h = VEC / 2; h > 0; h >>= 1)
+#pragma unroll
+        for (int i = 0; i < h; ++i) sum[i] += sum[i + h];
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) sum[0] += __shfl_xor(sum[0], o, 64);
+      if (lane == 0) dw[p] = sum[0];
     }
   } else if (dw && lane == 0) {
     dw[p] = 0.0f;
