@@ -71,3 +71,35 @@ def test_weight_gradients_of_random_rows(K, d, dtype):
     dy, rows = (torch.randn(130, d, generator=g).to(DT[dtype]).double() for _ in range(2))
     ref, mag = (dy * rows).sum(1), (dy * rows).abs().sum(1)
     assert ((dw_of(K, dy, rows, dtype) - ref).abs() <= (roundings(d, dtype) + 1) * 2.0 ** -24 * mag).all()
+
+
+# pairs in chunks of 2048 up to 2^20 pairs (128 chunks: the last number that every workgroup sums itself; 129 and
+# more: a launch of their own sums them), of 4096 above: 257 to the documented limits' 8192
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("t,k,e", [(131072, 2, 896), (131071, 2, 1024), (131073, 2, 1024), (262145, 1, 17), (100001, 5, 300),
+                                   (32768, 16, 896), (262144, 4, 1000), (1048576, 1, 1), (65537, 16, 896), (1048575, 3, 77)])
+def test_orders_of_many_chunks(K, t, k, e, dtype):
+    check_order(K, t, k, e, dtype)
+
+
+def test_the_order_of_the_most_pairs(K):
+    check_order(K, 1 << 20, 32, 1024, torch.int32)
+
+
+def check_order(K, t, k, e, dtype):
+    # experts of very different size, a sixth of the choices dropped, whole stretches of them too
+    rng = np.random.default_rng(t + k + e)
+    ids = np.minimum(rng.integers(0, e, (t, k)), rng.integers(0, e + e // 5 + 1, (t, k))).astype(np.int16)
+    ids[rng.random((t, k)) < 1 / 6] = -1
+    ids[t // 3:t // 3 + 3000] = e
+    flat = ids.reshape(-1)
+    kept = np.flatnonzero((flat >= 0) & (flat < e))
+    src = kept[np.argsort(flat[kept], kind="stable")]
+    order = K.sort_tokens(torch.from_numpy(ids).to(dtype).cuda(), e)
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(flat[kept], minlength=e))])
+    assert np.array_equal(order.offsets.cpu().numpy(), offsets)
+    row_src = order.row_src.cpu().numpy()
+    assert np.array_equal(row_src[:src.size], src) and (row_src[src.size:] == -1).all()
+    token_row = np.full(flat.size, -1, dtype=np.int32)
+    token_row[src] = np.arange(src.size, dtype=np.int32)
+    assert np.array_equal(order.token_row.cpu().numpy().reshape(-1), token_row)
