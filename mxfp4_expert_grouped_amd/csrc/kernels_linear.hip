@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "linear_choice.h"
 #include "row_types.h"
 
 namespace mxmoe {
@@ -367,7 +368,7 @@ __device__ __forceinline__ v16f mfma32_fp4(uint4 w, uint4 a, v16f c, uint32_t sw
                                                          static_cast<int>(sw), 2 * H, static_cast<int>(sa));
 }
 
-constexpr int kTileN = 256, kTileThreads = 256;
+constexpr int kTileThreads = 256;
 constexpr int kPanel = 4;  // row tiles that share a column block's weights in time
 
 template <int SZ, int BM, int GS>
@@ -795,21 +796,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   wait_vm<0>();
 }
 
-// Row tiles of bm rows: known for one matrix, otherwise an estimate (the
-// offsets are on the device): half a tile more per matrix than full ones, and
-// at least one for every row or matrix.
-int64_t row_tiles(const LinearArgs& a, int64_t bm) {
-  if (!a.offsets) return (a.rows + bm - 1) / bm;
-  return std::max<int64_t>((a.rows + bm - 1) / bm + a.mats / 2, std::min<int64_t>(a.rows, a.mats));
-}
-// at most so many
-int64_t row_tiles_max(const LinearArgs& a, int64_t bm) {
-  return a.offsets ? std::min<int64_t>(a.rows, (a.rows + bm - 1) / bm + a.mats) : (a.rows + bm - 1) / bm;
+LinearShape shape_of(const LinearArgs& a, int size) {
+  const int64_t sb = a.k / 32;
+  auto on = [&](int64_t al) { return rows_aligned(a.a_s, sb, al) && rows_aligned(a.w_s, sb, al); };
+  const bool pieces = rows_aligned(a.y, a.ld_y * size, 16) && a.n % (16 / size) == 0;
+  return {a.rows, a.n, a.k, a.mats, a.offsets != nullptr, size, a.ld_y * size, pieces, on(16) ? 16 : on(4) ? 4 : 1, a.num_cus};
 }
 
 template <typename T, int SCALES, int MT, int NB, int NW>
-hipError_t stream_v(const LinearArgs& a, hipStream_t st) {
-  const int64_t units = row_tiles_max(a, 16 * MT) * ((a.n + 16 * NB - 1) / (16 * NB));
+hipError_t stream_v(const LinearArgs& a, const LinearShape& s, hipStream_t st) {
+  const int64_t units = row_tiles_max(s, 16 * MT) * ((a.n + 16 * NB - 1) / (16 * NB));
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, (NW == 4 ? 8 : 2) * a.num_cus));
   // four columns of a row can be stored at once
   const bool wide = rows_aligned(a.y, a.ld_y * sizeof(T), 4 * sizeof(T));
@@ -818,71 +814,35 @@ hipError_t stream_v(const LinearArgs& a, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t stream_t(const LinearArgs& a, hipStream_t st) {
-  const int64_t sb = a.k / 32;
-  auto on = [&](int64_t al) { return rows_aligned(a.a_s, sb, al) && rows_aligned(a.w_s, sb, al); };
-  const bool one = row_tiles_max(a, 16) * ((a.n + 15) / 16) <= a.num_cus;
-  if (a.k % 512 == 0 && on(16)) return one ? stream_v<T, 0, 1, 1, 8>(a, st) : stream_v<T, 0, 1, 1, 4>(a, st);
-  if (a.k % 128 == 0 && on(4)) return one ? stream_v<T, 1, 1, 1, 8>(a, st) : stream_v<T, 1, 1, 1, 4>(a, st);
-  // what the tile kernel does not take comes here at every size: many rows in
-  // units of 64 x 32, which read half as much per product
-  return a.rows > 32 * a.mats ? stream_v<T, 2, 4, 2, 8>(a, st) : stream_v<T, 2, 1, 1, 4>(a, st);
+hipError_t stream_t(const LinearArgs& a, const LinearShape& s, const LinearChoice& c, hipStream_t st) {
+  if (c.scales == 0) return c.waves == 8 ? stream_v<T, 0, 1, 1, 8>(a, s, st) : stream_v<T, 0, 1, 1, 4>(a, s, st);
+  if (c.scales == 1) return c.waves == 8 ? stream_v<T, 1, 1, 1, 8>(a, s, st) : stream_v<T, 1, 1, 1, 4>(a, s, st);
+  return c.mt == 4 ? stream_v<T, 2, 4, 2, 8>(a, s, st) : stream_v<T, 2, 1, 1, 4>(a, s, st);
 }
 
 template <typename T, int BM>
-hipError_t tile_t(const LinearArgs& a, hipStream_t st) {
-  const int64_t sb = a.k / 32;
-  const bool wide = rows_aligned(a.y, a.ld_y * sizeof(T), 16) && a.n % (16 / sizeof(T)) == 0;
-  // (256 rows of fp32 and partial pieces need more registers than there are;
-  // with 16-bit results they fit: 8192 x 4095, k = 7168, 160 us against 197 us
-  // in tiles of 128 rows)
-  if constexpr (BM == 256 && sizeof(T) == 4)
-    if (!wide) return tile_t<T, 128>(a, st);
-  const bool pieces = a.k % 512 == 0 && rows_aligned(a.a_s, sb, 16) && rows_aligned(a.w_s, sb, 16);
-  const bool once = a.rows <= (a.offsets ? 32 * a.mats : 64);
-  const int64_t tiles = row_tiles_max(a, BM) * ((a.n + kTileN - 1) / kTileN);
+hipError_t tile_t(const LinearArgs& a, const LinearShape& s, const LinearChoice& c, hipStream_t st) {
+  const int64_t tiles = row_tiles_max(s, BM) * ((a.n + kTileN - 1) / kTileN);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, a.num_cus));
   auto go = [&](auto k) {
     k<<<grid, kTileThreads, 0, st>>>(a);
     return hipGetLastError();
   };
   if constexpr (BM != 256 || sizeof(T) != 4)
-    if (!wide) return go(k_linear_tile<T, BM, 0, false, false>);
+    if (!c.wide) return go(k_linear_tile<T, BM, 0, false, false>);
   if constexpr (BM == 64) {
-    if (pieces && a.k % 1024 == 0)
-      return once ? go(k_linear_tile<T, BM, 4, true, true>) : go(k_linear_tile<T, BM, 4, true, false>);
-    if (once) return pieces ? go(k_linear_tile<T, BM, 2, true, true>) : go(k_linear_tile<T, BM, 0, true, true>);
+    if (c.scales == 4) return c.once ? go(k_linear_tile<T, BM, 4, true, true>) : go(k_linear_tile<T, BM, 4, true, false>);
+    if (c.once) return c.scales ? go(k_linear_tile<T, BM, 2, true, true>) : go(k_linear_tile<T, BM, 0, true, true>);
   }
-  return pieces ? go(k_linear_tile<T, BM, 2, true, false>) : go(k_linear_tile<T, BM, 0, true, false>);
+  return c.scales ? go(k_linear_tile<T, BM, 2, true, false>) : go(k_linear_tile<T, BM, 0, true, false>);
 }
 
-// Which kernel, by estimates of their times in units of 0.1 us.
-// Tiles: a tile on every CU takes 2 us and, per step of 256 of K,
-// 0.6, 0.8 and 1.3 us for 64, 128 and 256 rows when few CUs are busy; a full
-// chip takes about twice that for each (measured with k = 7168: 256 rows x
-// 4096 columns in 64 tiles of 64 rows 23 us, in 16 of 256 rows 38 us; 131072
-// rows over 64 matrices in 256-row tiles 314 us, in 64-row tiles 465 us), so
-// the same weights rank them in both cases.
-// Stream: 2 us, and 0.25 us per 256 units and 512 of K (measured: 64 rows x
-// 4096 columns, k = 7168, 16.8 us against 19.6 us in tiles; 128 rows 30
-// against 22 us; 16 rows 10 against 18 us).
 template <typename T>
 hipError_t linear_t(const LinearArgs& a, hipStream_t st) {
-  const int64_t sb = a.k / 32;
-  // (the tile kernel's stores reach 2^31 bytes from a tile's first row)
-  if (a.k % 128 || !rows_aligned(a.a_s, sb, 4) || !rows_aligned(a.w_s, sb, 4) ||
-      a.ld_y * sizeof(T) * 256 > (int64_t(1) << 31))
-    return stream_t<T>(a, st);
-  const int64_t cblocks = (a.n + kTileN - 1) / kTileN, steps = (a.k + 255) / 256;
-  auto tile_cost = [&](int64_t bm, int64_t step) {
-    return (row_tiles(a, bm) * cblocks + a.num_cus - 1) / a.num_cus * (20 + steps * step);
-  };
-  const int64_t c64 = tile_cost(64, 6), c128 = tile_cost(128, 8), c256 = tile_cost(256, 13);
-  const int64_t units = row_tiles(a, 16) * ((a.n + 15) / 16);
-  const int64_t stream = 20 + units * ((a.k + 511) / 512) * 25 / 2560;
-  const int64_t least = std::min(c64, std::min(c128, c256));
-  if (stream < least) return stream_t<T>(a, st);
-  return least == c64 ? tile_t<T, 64>(a, st) : least == c128 ? tile_t<T, 128>(a, st) : tile_t<T, 256>(a, st);
+  const LinearShape s = shape_of(a, sizeof(T));
+  const LinearChoice c = choose_linear(s);
+  if (c.bm == 0) return stream_t<T>(a, s, c, st);
+  return c.bm == 64 ? tile_t<T, 64>(a, s, c, st) : c.bm == 128 ? tile_t<T, 128>(a, s, c, st) : tile_t<T, 256>(a, s, c, st);
 }
 
 }  // namespace
