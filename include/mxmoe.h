@@ -274,7 +274,8 @@ moe_status moe_router_bias_update(const moe_plan_t *plan, const int32_t *expert_
  * Gradients there are of dispatch (moe_combine_rows without weights) and of
  * combine (moe_combine_rows_backward); none of the MXFP4 conversions and of
  * their product.
- * Errors and streams as for moe_forward.  What device memory holds (ids, row
+ * Errors and streams as for moe_forward; a call's outputs overlap none of its
+ * inputs.  What device memory holds (ids, row
  * numbers, offsets) cannot be checked on the host: values outside their range
  * are treated as said at each call and never reach outside a buffer. */
 
@@ -353,7 +354,7 @@ moe_status moe_sort_tokens(const void *ids, moe_id_dtype id_dt, int64_t num_toke
  * leave either copy.  num_rows (one int32 on the device, moe_sort_tokens'
  * offsets + num_experts) or NULL: rows from *num_rows on are zero-filled, with
  * NULL rows that no pair has are left as they were.  num_tokens == 0 or
- * row_bytes == 0 enqueues nothing.  x and xs must not overlap. */
+ * row_bytes == 0 enqueues nothing. */
 moe_status moe_dispatch_rows(const void *x, int64_t row_bytes, int64_t ld_x,
                              const int32_t *token_row, int64_t num_tokens, int32_t top_k,
                              const int32_t *num_rows, int64_t rows_cap, void *xs, int64_t ld_xs,
