@@ -177,7 +177,9 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 4 : 2) k_linear_stream(Line
   };
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     // (a 64-bit division takes a tenth of a short call)
-    const int t = static_cast<int>(units < (int64_t(1) << 31) ? static_cast<uint32_t>(u) / static_cast<uint32_t>(cblocks) : u / cblocks), cb = static_cast<int>(u - int64_t(t) * cblocks);
+    const int t = static_cast<int>(units < (int64_t(1) << 31) ? static_cast<uint32_t>(u) / static_cast<uint32_t>(cblocks)
+                                                              : u / cblocks);
+    const int cb = static_cast<int>(u - int64_t(t) * cblocks);
     const int e = tile_matrix(prefix, a.mats, t);
     int lo, hi;
     mat_rows(a, e, lo, hi);
@@ -439,7 +441,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
     const uint32_t local = pos - p0 * ntn, pn = kPanel * ntn;
     const int panel = __builtin_amdgcn_readfirstlane(static_cast<int>(local / pn)), within = local - panel * pn;
     const int gm = min(kPanel, p1 - p0 - panel * kPanel);
-    const int nt = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(within) / static_cast<uint32_t>(gm))), mt = panel * kPanel + within - nt * gm;
+    const int nt = __builtin_amdgcn_readfirstlane(
+        static_cast<int>(static_cast<uint32_t>(within) / static_cast<uint32_t>(gm)));
+    const int mt = panel * kPanel + within - nt * gm;
     int lo = 0, hi = static_cast<int>(a.rows);
     if (a.offsets) {
       sload2(a.offsets + t.e, lo, hi);

@@ -156,7 +156,6 @@ def _check(status: int):
         raise MoeError(status, load_library().moe_last_error().decode())
 
 
-
 def moe_plan(d_model: int, d_ff: int, num_experts: int, top_k: int, num_shared: int,
              max_tokens: int, flags: int = 0) -> c_void_p:
     cfg = MoeConfig(d_model, d_ff, num_experts, top_k, num_shared, max_tokens, flags)
