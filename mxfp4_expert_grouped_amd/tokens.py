@@ -42,7 +42,9 @@ class TokenOrder:
         if offsets.numel() < 2 or row_src.numel() != token_row.numel():
             raise ValueError(f"offsets {list(offsets.shape)}, row_src {list(row_src.shape)} and token_row "
                              f"{list(token_row.shape)} are not [E+1], [T*k] and [T, k]")
-        _fill(self, offsets, row_src, token_row)
+        _set_offsets(self, offsets)      # int32 [E+1] first row of each expert; offsets[E] rows in all
+        _set_row_src(self, row_src)      # int32 [T*k] pair t*k + j of each row, -1 behind the last
+        _set_token_row(self, token_row)  # int32 [T, k] row of each pair, -1 for a dropped one
 
     def __setattr__(self, name, value):
         raise AttributeError("a TokenOrder does not change: make another one")
@@ -75,16 +77,16 @@ class TokenOrder:
 _set_offsets, _set_row_src, _set_token_row = (TokenOrder.__dict__[n].__set__ for n in TokenOrder.__slots__)
 
 
-def _fill(order: TokenOrder, offsets: torch.Tensor, row_src: torch.Tensor, token_row: torch.Tensor) -> TokenOrder:
-    _set_offsets(order, offsets)      # int32 [E+1] first row of each expert; offsets[E] rows in all
-    _set_row_src(order, row_src)      # int32 [T*k] pair t*k + j of each row, -1 behind the last
-    _set_token_row(order, token_row)  # int32 [T, k] row of each pair, -1 for a dropped one
-    return order
+_new = TokenOrder.__new__
 
 
-def _own_order(*tensors: torch.Tensor) -> TokenOrder:
+def _own_order(offsets: torch.Tensor, row_src: torch.Tensor, token_row: torch.Tensor) -> TokenOrder:
     """An order of tensors made here (the checks take a tenth of a small call)."""
-    return _fill(object.__new__(TokenOrder), *tensors)
+    order = _new(TokenOrder)
+    _set_offsets(order, offsets)
+    _set_row_src(order, row_src)
+    _set_token_row(order, token_row)
+    return order
 
 
 _sort_workspace = lru_cache(maxsize=256)(M.moe_sort_tokens_workspace_bytes)
@@ -144,7 +146,7 @@ def _combine(rows: torch.Tensor, weights: Optional[torch.Tensor], order: TokenOr
     t, k = tr.shape
     rows, ld = _matrix(rows, t * k, "rows")
     if weights is not None:
-        weights = in_memory(weights).contiguous()
+        weights = (weights.resolve_neg() if weights.is_neg() else weights).contiguous()
     d = rows.shape[1]
     y = torch.empty(t, d, dtype=rows.dtype, device=rows.device)
     on_device(dev, M.moe_combine_rows, rows.data_ptr(), row_dtype(rows.dtype), t * k, d, ld, tr.data_ptr(),
@@ -175,7 +177,7 @@ def combine_backward(dy: torch.Tensor, rows: Optional[torch.Tensor], weights: Op
     if rows is not None:
         rows, ld_rows = _matrix(rows, t * k, "rows")
     if weights is not None:
-        weights = in_memory(weights).contiguous()
+        weights = (weights.resolve_neg() if weights.is_neg() else weights).contiguous()
     drows = torch.empty(t * k, d, dtype=dy.dtype, device=dy.device) if need_rows else None
     dw = torch.empty(t, k, dtype=torch.float32, device=dy.device) if need_weights else None
     ptr = lambda x: x.data_ptr() if x is not None else None  # noqa: E731
