@@ -124,6 +124,19 @@ def test_every_variant(L, rows, n, k, dtype):
         at += c
 
 
+@pytest.mark.parametrize("rows,n,k", [(40, 56, 96), (600, 2056, 2016), (2048, 4096, 2880)])
+def test_zero_blocks_at_the_end_of_k_add_nothing(L, rows, n, k):
+    # a k that tiles do not take, padded to one that they take: held to the bound of the sum without the padding
+    g = torch.Generator(device="cuda").manual_seed(k)
+    ac, asc = random_mx4((rows,), k, g)
+    wc, wsc = random_mx4((n,), k, g)
+    more = -k % 128
+    pad = torch.nn.functional.pad
+    y = L.linear_mx4(pad(ac, (0, more // 2)), pad(asc, (0, more // 32)), pad(wc, (0, more // 2)), pad(wsc, (0, more // 32)),
+                     dtype=torch.float32)
+    assert_product(y, values(ac, asc), values(wc, wsc), k, "fp32")
+
+
 @pytest.mark.parametrize("rows,n,k", [(3, 40, 512), (70, 40, 96), (600, 8192, 512), (600, 8191, 384)])
 @pytest.mark.parametrize("ld", [(1 << 22) - 8, 1 << 22, (1 << 22) + 8])
 def test_rows_of_y_far_apart(L, rows, n, k, ld):
