@@ -288,16 +288,17 @@ __global__ void __launch_bounds__(64 * NW, NW == 4 ? 4 : 2) k_linear_stream(Line
 // = 4 (k % 1024 == 0; 64-row tiles, whose rows are many for their products)
 // or 2 (k % 512 == 0), scale rows on 16 bytes; GS = 0 otherwise: two dwords
 // per row and step, in the slot.  The number of pieces matters more than their
-// bytes: 4096 rows over 64 matrices of 4096 x 7168 take 213 us without any,
-// 243 us with GS = 2.  A dword holds half a step's scales, byte 2q + g32 that
+// bytes: in one comparison 4096 rows over 64 matrices of 4096 x 7168 took 213 us
+// without any (and wrong results), 243 us with GS = 2.  A dword holds half a step's scales, byte 2q + g32 that
 // of its quarter q of lane (l32, g32): shifted by 8 g32 once per step, the
 // MFMA takes byte 2q.
 //
-// Measured: 8192 x 4096, k = 7168, 114 us (4.2 PF; the matrix cores busy 54 % of
-// the cycles at 1.87 GHz: the clock falls with the power that MFMAs and copies
-// draw together, 2.4 GHz without copies); 131072 rows over 64 matrices of 7168
-// x 2048 1.14 ms (3.4 PF), of which 0.26 ms are the stores of y; 16 rows for 16
-// of 64 matrices of 4096 x 7168 41.6 us (6.0 TB/s of weights).
+// Measured (medians of single calls): 8192 x 4096, k = 7168, 112 us (4.3 PF; the
+// matrix cores busy 54 % of the cycles, at a clock of 1.9 GHz); 131072 rows over
+// 64 matrices of 7168 x 2048 1.15 ms in a row of calls, 1.22 ms among pauses
+// (3.3 PF; busy 49 %, 1.35 to 1.65 GHz): a tile's results are stored while no
+// MFMA runs; 16 rows for 16 of 64 matrices of 4096 x 7168 41.8 us (6.0 TB/s of
+// weights).
 //
 // With k % 256 == 128 a row's last step is half a step: its copies bring the
 // first 64 bytes twice, and it has two quarters.  Rows past the tile's or the
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_linear_tile(LinearArgs a) {
   // (which would cost copies of the accumulators).  Otherwise the same 16-byte
   // pieces at any address, and only a row's last one by elements (8192 x 4095,
   // k = 2048, bf16: 66 us, 121 us with every element on its own; 4096 columns
-  // 40 us, all of it whole cache lines).
+  // 44 us).
   constexpr uint32_t kNowhere = 0x80000000u;  // the buffer ends here
   auto store_tile = [&](const TileAt& t) {
     constexpr int SZ = sizeof(T), PER = 16 / SZ;
