@@ -30,7 +30,9 @@ FLAGS = [
 
 LIBS = {
     "libmxmoe.so": ["api.cpp", "kernels_route.hip", "kernels_gemm.hip", "kernels_pack.hip",
-                    "kernels_tail.hip", "kernels_mx4.hip", "kernels_linear.hip", "kernels_tokens.hip"],
+                    "kernels_tail.hip", "kernels_mx4.hip", "kernels_linear.hip", "kernels_tokens.hip",
+                    "kernels_rows_forward.hip", "kernels_rows_input.hip", "kernels_rows_weight.hip",
+                    "kernels_rows_aux.hip"],
     "libmxmoe_inputs.so": ["gen_inputs.hip"],
 }
 

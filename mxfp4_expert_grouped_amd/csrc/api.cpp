@@ -14,6 +14,7 @@
 
 #include "../../include/mxmoe.h"
 #include "internal.h"
+#include "rows_choice.h"
 
 using namespace mxmoe;
 
@@ -842,6 +843,174 @@ moe_status moe_combine_rows_backward(const void* dy, const void* rows, moe_src_d
   a.drows = drows; a.ld_d = ld_drows;
   a.dw = dw; a.num_rows = num_rows;
   return launched(launch_combine_rows_backward(a, t, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// 16-bit products of rows sorted by expert
+// ---------------------------------------------------------------------------
+namespace {
+
+using rows::Pass;
+
+// One product as its entry point was called: sizes, row strides (elements)
+// and the pieces of its workspace.
+struct RowsCall {
+  rows::RowsShape s;
+  rows::RowsChoice c;
+  // operands that are laid out in the workspace first, rows on 16 bytes
+  bool pad_a, pad_b;
+  int64_t ld_a, ld_b;                // row strides of the operands as the kernels read them
+  size_t off_a, off_b, off_part, total;
+};
+
+// Checks of what does not depend on pointers; -> the call's layout.  a: x or
+// dy, ld_a apart; for the weights' gradient ld_x is the stride of x.
+moe_status plan_rows(moe_rows_pass pass, moe_src_dtype dt, int64_t nrows, int64_t ld_a, int64_t ld_x, int32_t mats, bool grouped,
+                     int64_t n, int64_t k, moe_src_dtype out_dt, int64_t ld_out, RowsCall& p) {
+  if (pass != MOE_ROWS_FORWARD && pass != MOE_ROWS_INPUT && pass != MOE_ROWS_WEIGHT) return fail(MOE_ERR_INVALID_ARG, "bad pass");
+  if (dt != MOE_SRC_BF16 && dt != MOE_SRC_FP16)
+    return fail(dt == MOE_SRC_FP32 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG, "the products take bf16 and fp16");
+  if (out_dt != dt && !(pass == MOE_ROWS_WEIGHT && out_dt == MOE_SRC_FP32)) return fail(MOE_ERR_INVALID_ARG, "bad type of the result");
+  if (nrows < 0 || n < 0 || k < 0 || mats <= 0) return fail(MOE_ERR_INVALID_ARG, "negative size, or mats not positive");
+  if (!grouped && mats != 1) return fail(MOE_ERR_INVALID_ARG, "%d matrices need offsets", mats);
+  if (mats > rows::kMaxRowMats || n > (1 << 20) || k > (1 << 20) || nrows > (1 << 25))
+    return fail(MOE_ERR_UNSUPPORTED, "more than 1024 matrices, 2^20 columns or 2^25 rows");
+  const int64_t wa = pass == MOE_ROWS_FORWARD ? k : n, wo = pass == MOE_ROWS_FORWARD ? n : k;
+  if (ld_a < wa || (pass == MOE_ROWS_WEIGHT && ld_x < k) || (pass != MOE_ROWS_WEIGHT && ld_out < wo))
+    return fail(MOE_ERR_INVALID_ARG, "row stride below the row's width");
+  if (ld_a > (1 << 21) || ld_x > (1 << 21) || ld_out > (1 << 21)) return fail(MOE_ERR_UNSUPPORTED, "row stride above 2^21");
+  const int64_t tn = rows::ceil_div(wo, rows::kRowsTileN);
+  const int64_t tiles = pass == MOE_ROWS_WEIGHT ? mats * rows::ceil_div(n, 128) * tn : (rows::ceil_div(nrows, 64) + mats) * tn;
+  if (tiles > rows::kMaxRowTiles) return fail(MOE_ERR_UNSUPPORTED, "more than 2^30 tiles");
+  const int osz = out_dt == MOE_SRC_FP32 ? 4 : 2;
+  p.s = {pass == MOE_ROWS_FORWARD ? Pass::kForward : pass == MOE_ROWS_INPUT ? Pass::kInput : Pass::kWeight,
+         nrows, n, k, mats, grouped, osz, wo % (16 / osz) == 0 && ld_out % (16 / osz) == 0};
+  p.c = rows::choose_rows(p.s);
+  // rows of whole pieces of 16 bytes are read where they are
+  p.pad_a = wa % 8 || ld_a % 8;
+  p.pad_b = pass == MOE_ROWS_WEIGHT ? (k % 8 || ld_x % 8) : k % 8 != 0;
+  p.ld_a = p.pad_a ? rows::round8(wa) : ld_a;
+  p.ld_b = p.pad_b ? rows::round8(k) : pass == MOE_ROWS_WEIGHT ? ld_x : k;
+  size_t at = 0;
+  auto take = [&](bool used, int64_t bytes) {
+    const size_t o = at;
+    if (used) at += (size_t(bytes) + 255) & ~size_t(255);
+    return o;
+  };
+  p.off_a = take(p.pad_a, nrows * p.ld_a * 2);
+  p.off_b = take(p.pad_b, (pass == MOE_ROWS_WEIGHT ? nrows : mats * n) * p.ld_b * 2);
+  p.off_part = take(p.c.join, rows::join_rows(p.s) * rows::join_ld(p.s) * p.c.slices * 4);
+  p.total = at;
+  return MOE_OK;
+}
+
+// Runs the product: a as above, b is w or x.
+moe_status run_rows(RowsCall& p, moe_src_dtype dt, const void* a, int64_t ld_a, const void* b, int64_t ld_b, const int32_t* offsets,
+                    void* out, moe_src_dtype out_dt, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
+  const rows::RowsShape& s = p.s;
+  const bool weight = s.pass == Pass::kWeight;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, s.out_size) || !aligned(offsets, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer (operands: 16 bytes; offsets: 4; the result: its element, 16 bytes as fp32)");
+  if (s.out_size == 4 && !aligned(out, 16)) return fail(MOE_ERR_INVALID_ARG, "an fp32 result needs 16-byte alignment");
+  if (p.total && (!workspace || workspace_bytes < p.total))
+    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s", p.total, workspace_bytes, workspace ? "" : " (NULL)");
+  if (p.total && !aligned(workspace, 256)) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  int num_cus = 0;
+  moe_status st = check_device(&num_cus);
+  if (st != MOE_OK) return st;
+  if (!p.c.join && s.pieces && !aligned(out, 16)) p.c.wide = false;
+  RowType t, ot;
+  int64_t sz;
+  row_type(dt, t, sz);
+  row_type(out_dt, ot, sz);
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  hipError_t e = hipSuccess;
+  if (p.pad_a) {
+    e = rows::launch_pad_rows(a, s.rows, s.pass == Pass::kForward ? s.k : s.n, ld_a, ws + p.off_a, p.ld_a, hs);
+    a = ws + p.off_a;
+  }
+  if (p.pad_b && e == hipSuccess) {
+    e = rows::launch_pad_rows(b, weight ? s.rows : s.mats * s.n, s.k, ld_b, ws + p.off_b, p.ld_b, hs);
+    b = ws + p.off_b;
+  }
+  if (e != hipSuccess) return launched(e);
+  const int64_t cols = s.cols();
+  rows::RowsArgs r{};
+  r.a = a; r.ld_a = p.ld_a;
+  r.b = b; r.ld_b = p.ld_b; r.mat_b = s.n * p.ld_b;
+  r.offsets = offsets; r.rows = s.rows; r.mats = s.mats;
+  r.m = static_cast<int>(s.n);
+  r.n = static_cast<int>(cols);
+  r.l = static_cast<int>(s.pass == Pass::kForward ? s.k : s.n);
+  r.slices = p.c.slices;
+  r.num_cus = num_cus > 0 ? num_cus : 256;
+  if (p.c.join) {
+    r.c = ws + p.off_part;
+    r.ld_c = rows::join_ld(s);
+    r.slice_c = rows::join_rows(s) * r.ld_c;
+  } else {
+    r.c = out;
+    r.ld_c = ld_out;
+  }
+  r.mat_c = s.n * r.ld_c;
+  const RowType ct = p.c.join ? RowType::kFp32 : ot;
+  switch (s.pass) {
+    case Pass::kForward: e = rows::launch_forward(r, p.c, t, ct, hs); break;
+    case Pass::kInput: e = rows::launch_input(r, p.c, t, ct, hs); break;
+    default: e = rows::launch_weight(r, p.c, t, ct, hs);
+  }
+  if (e == hipSuccess && p.c.join)
+    e = rows::launch_join(static_cast<const float*>(r.c), p.c.slices, rows::join_rows(s), cols, r.ld_c, weight ? nullptr : offsets,
+                          s.mats, out, ot, ld_out, hs);
+  return launched(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_linear_rows_workspace_bytes(moe_rows_pass pass, moe_src_dtype dt, int64_t num_rows, int64_t ld_a, int64_t ld_x,
+                                           int32_t mats, int32_t grouped, int64_t n, int64_t k, moe_src_dtype out_dt, int64_t ld_out,
+                                           size_t* out_bytes) {
+  if (!out_bytes) return fail(MOE_ERR_INVALID_ARG, "out_bytes is NULL");
+  RowsCall p;
+  moe_status s = plan_rows(pass, dt, num_rows, ld_a, ld_x, mats, grouped != 0, n, k, out_dt, ld_out, p);
+  if (s != MOE_OK) return s;
+  *out_bytes = p.total;
+  return MOE_OK;
+}
+
+moe_status moe_linear_rows(const void* x, moe_src_dtype dt, int64_t num_rows, int64_t ld_x, const void* w, int32_t mats,
+                           const int32_t* offsets, int64_t n, int64_t k, void* y, int64_t ld_y, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  RowsCall p;
+  moe_status s = plan_rows(MOE_ROWS_FORWARD, dt, num_rows, ld_x, 0, mats, offsets != nullptr, n, k, dt, ld_y, p);
+  if (s != MOE_OK || num_rows == 0 || n == 0) return s;
+  if (!y || (k > 0 && (!x || !w))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  return run_rows(p, dt, x, ld_x, w, k, offsets, y, dt, ld_y, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_linear_rows_dx(const void* dy, moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, const void* w, int32_t mats,
+                              const int32_t* offsets, int64_t n, int64_t k, void* dx, int64_t ld_dx, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  RowsCall p;
+  moe_status s = plan_rows(MOE_ROWS_INPUT, dt, num_rows, ld_dy, 0, mats, offsets != nullptr, n, k, dt, ld_dx, p);
+  if (s != MOE_OK || num_rows == 0 || k == 0) return s;
+  if (!dx || (n > 0 && (!dy || !w))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  return run_rows(p, dt, dy, ld_dy, w, k, offsets, dx, dt, ld_dx, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_linear_rows_dw(const void* dy, moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, const void* x, int64_t ld_x,
+                              int32_t mats, const int32_t* offsets, int64_t n, int64_t k, void* dw, moe_src_dtype dw_dt,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  RowsCall p;
+  moe_status s = plan_rows(MOE_ROWS_WEIGHT, dt, num_rows, ld_dy, ld_x, mats, offsets != nullptr, n, k, dw_dt, k, p);
+  if (s != MOE_OK || n == 0 || k == 0) return s;
+  if (!dw || (num_rows > 0 && (!dy || !x))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  return run_rows(p, dt, dy, ld_dy, x, ld_x, offsets, dw, dw_dt, k, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -225,6 +225,39 @@ struct CombineArgs {
 hipError_t launch_combine_rows(const CombineArgs& a, RowType dt, hipStream_t st);
 hipError_t launch_combine_rows_backward(const CombineArgs& a, RowType dt, hipStream_t st);
 
+// ---- 16-bit products of rows sorted by expert (rows_choice.h, rows_tile.h)
+namespace rows {
+enum class Pass;
+struct RowsChoice;
+
+struct RowsArgs {
+  const void* a;             // the side of C's rows: x [rows][ld_a], dy [rows][ld_a]
+  int64_t ld_a;
+  const void* b;             // the side of C's columns: W [mats][mat_b], its rows ld_b apart, or x [rows][ld_b]
+  int64_t ld_b, mat_b;
+  const int* offsets;        // [mats+1] first row of each matrix, or null: all rows to one matrix
+  int64_t rows;
+  int mats;
+  int m, n, l;               // C's rows (weights' gradient), its columns, the length of the sums (else)
+  void* c;                   // [rows][ld_c], or [mats][mat_c] with rows of ld_c; slice s from s * slice_c on
+  int64_t ld_c, mat_c, slice_c;
+  int slices;
+  int num_cus;
+};
+// both operands on 16 bytes with rows on 16 bytes, what they hold between a
+// row's end and its next 16 bytes zero
+hipError_t launch_forward(const RowsArgs& a, const RowsChoice& c, RowType in, RowType out, hipStream_t st);
+hipError_t launch_input(const RowsArgs& a, const RowsChoice& c, RowType in, RowType out, hipStream_t st);
+hipError_t launch_weight(const RowsArgs& a, const RowsChoice& c, RowType in, RowType out, hipStream_t st);
+
+// dst [rows][ld_dst] = src [rows][ld_src] (16-bit elements), zeros from cols to ld_dst
+hipError_t launch_pad_rows(const void* src, int64_t rows, int64_t cols, int64_t ld_src, void* dst, int64_t ld_dst,
+                           hipStream_t st);
+// out[r] = sum of the slices' row r, rounded once; with offsets, rows of no matrix are zero
+hipError_t launch_join(const float* part, int slices, int64_t rows, int64_t cols, int64_t ld, const int* offsets, int mats,
+                       void* out, RowType out_t, int64_t ld_out, hipStream_t st);
+}  // namespace rows
+
 // bytes of one packed scale matrix [rows/16][ceil(k/512)][64][4]
 __host__ __device__ inline int64_t packed_scale_bytes(int64_t rows, int64_t k) { return rows * (k / 32); }
 

@@ -1,0 +1,93 @@
+// What stands around the 16-bit products of rows: rows laid out on 16 bytes,
+// and fp32 sums of parts joined.  Both are bound by memory.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "row_types.h"
+
+namespace mxmoe {
+namespace rows {
+
+namespace {
+
+constexpr int kAuxThreads = 256;
+// grid of at most 2^31 threads; the kernels stride over the rest
+inline unsigned aux_grid(int64_t n) { return static_cast<unsigned>(std::min<int64_t>((n + kAuxThreads - 1) / kAuxThreads, 1 << 23)); }
+
+// A thread moves one piece of 16 bytes of dst.
+__global__ void __launch_bounds__(kAuxThreads) k_pad_rows(const uint16_t* __restrict__ src, int64_t pieces, int cols, int64_t ld_src,
+                                                          uint16_t* __restrict__ dst, int per_row) {
+  for (int64_t p = int64_t(blockIdx.x) * kAuxThreads + threadIdx.x; p < pieces; p += int64_t(gridDim.x) * kAuxThreads) {
+    const int64_t row = pieces < (int64_t(1) << 31) ? static_cast<uint32_t>(p) / static_cast<uint32_t>(per_row) : p / per_row;
+    const int col = 8 * static_cast<int>(p - row * per_row);
+    const uint16_t* s = src + row * ld_src + col;
+    u32x4 v;
+    if (col + 8 <= cols) {
+      v = load16<false, false, u32x4>(s);
+    } else {
+      v = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col + i < cols) v[i / 2] |= static_cast<uint32_t>(s[i]) << (16 * (i % 2));
+    }
+    reinterpret_cast<u32x4*>(dst)[p] = v;
+  }
+}
+
+// A thread sums four columns over the slices, in their order.
+template <typename T>
+__global__ void __launch_bounds__(kAuxThreads) k_join(const float* __restrict__ part, int slices, int64_t slice, int64_t quads,
+                                                      int per_row, int cols, const int* __restrict__ offsets, int mats, int64_t rows,
+                                                      T* __restrict__ out, int64_t ld_out) {
+  int64_t lo = 0, hi = rows;
+  if (offsets) {  // rows of no matrix have no sums
+    lo = min(max(int64_t(offsets[0]), int64_t(0)), rows);
+    hi = max(lo, min(max(int64_t(offsets[mats]), int64_t(0)), rows));
+  }
+  for (int64_t p = int64_t(blockIdx.x) * kAuxThreads + threadIdx.x; p < quads; p += int64_t(gridDim.x) * kAuxThreads) {
+    const int64_t row = quads < (int64_t(1) << 31) ? static_cast<uint32_t>(p) / static_cast<uint32_t>(per_row) : p / per_row;
+    const int col = 4 * static_cast<int>(p - row * per_row);
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (row >= lo && row < hi) {
+      for (int i = 0; i < slices; ++i) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(part + i * slice + 4 * p);
+        s[0] += v[0]; s[1] += v[1]; s[2] += v[2]; s[3] += v[3];
+      }
+    }
+    T* o = out + row * ld_out + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < cols) o[i] = from_f32<T>(s[i]);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_pad_rows(const void* src, int64_t rows, int64_t cols, int64_t ld_src, void* dst, int64_t ld_dst, hipStream_t st) {
+  const int64_t pieces = rows * (ld_dst / 8);
+  if (pieces == 0) return hipSuccess;
+  k_pad_rows<<<aux_grid(pieces), kAuxThreads, 0, st>>>(static_cast<const uint16_t*>(src), pieces, static_cast<int>(cols), ld_src,
+                                                       static_cast<uint16_t*>(dst), static_cast<int>(ld_dst / 8));
+  return hipGetLastError();
+}
+
+hipError_t launch_join(const float* part, int slices, int64_t rows, int64_t cols, int64_t ld, const int* offsets, int mats,
+                       void* out, RowType out_t, int64_t ld_out, hipStream_t st) {
+  const int64_t quads = rows * (ld / 4);
+  auto go = [&](auto* o) {
+    k_join<<<aux_grid(quads), kAuxThreads, 0, st>>>(part, slices, rows * ld, quads, static_cast<int>(ld / 4), static_cast<int>(cols),
+                                                    offsets, mats, rows, o, ld_out);
+    return hipGetLastError();
+  };
+  switch (out_t) {
+    case RowType::kBf16: return go(static_cast<bf16_t*>(out));
+    case RowType::kFp16: return go(static_cast<_Float16*>(out));
+    default: return go(static_cast<float*>(out));
+  }
+}
+
+}  // namespace rows
+}  // namespace mxmoe

@@ -1,0 +1,91 @@
+// Which kernel a 16-bit product of rows sorted by expert takes, and what its
+// workspace holds: the rules alone, plain host code without a device.
+#pragma once
+
+#include <stdint.h>
+
+#include <algorithm>
+
+namespace mxmoe {
+namespace rows {
+
+// y = x W^T; dx = dy W; dW = dy^T x
+enum class Pass { kForward, kInput, kWeight };
+
+constexpr int kMaxRowMats = 1024;
+constexpr int kRowsTileN = 256;  // columns of a tile
+// Output tiles that a launch counts to, and how many a product may have: in
+// tiles of 64 rows (the lowest) x 256 columns, one more per matrix for its end.
+constexpr int64_t kMaxRowTiles = int64_t(1) << 30;
+constexpr int kCus = 256;        // compute units that the estimates below count with
+constexpr int kMaxSlices = 64;
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round8(int64_t v) { return (v + 7) & ~int64_t(7); }
+
+// The product as the tile kernel sees it: C [m x n], sums over l
+struct RowsShape {
+  Pass pass;
+  int64_t rows, n, k;   // of the operator: rows, W [mats][n][k]
+  int mats;
+  bool grouped;         // rows go to the matrices by offsets, else all to the one
+  int out_size;         // bytes of an element of C
+  bool pieces;          // a row of C is a whole number of 16-byte pieces, on 16 bytes
+
+  int64_t cols() const { return pass == Pass::kForward ? n : k; }
+  int64_t length() const { return pass == Pass::kForward ? k : pass == Pass::kInput ? n : rows / std::max(1, mats); }
+  // row tiles of bm rows: known for one matrix and for the weights' gradient,
+  // otherwise an estimate (the offsets are on the device): half a tile more per
+  // matrix than full ones, and at least one for every row or matrix
+  int64_t row_tiles(int64_t bm) const {
+    if (pass == Pass::kWeight) return mats * ceil_div(n, bm);
+    if (!grouped) return ceil_div(rows, bm);
+    return std::max<int64_t>(ceil_div(rows, bm) + mats / 2, std::min<int64_t>(rows, mats));
+  }
+  // at most so many
+  int64_t row_tiles_max(int64_t bm) const {
+    if (pass == Pass::kWeight || !grouped) return row_tiles(bm);
+    return std::min<int64_t>(rows, ceil_div(rows, bm) + mats);
+  }
+};
+
+struct RowsChoice {
+  bool stream;     // k_rows_stream, else k_rows_tile:
+  int bm;          // rows of a tile, 64 (not for the weights' gradient), 128 or 256
+  int slices;      // parts of L, joined from fp32 sums in the workspace
+  bool join;       // through the workspace (slices > 1, or rows that the tile kernel cannot write)
+  bool wide;       // rows of C in whole pieces
+  int64_t tiles;   // at most so many, slices counted
+};
+
+// fp32 sums of a slice: rows of C as the tile kernel writes them
+inline int64_t join_rows(const RowsShape& s) { return s.pass == Pass::kWeight ? s.mats * s.n : s.rows; }
+inline int64_t join_ld(const RowsShape& s) { return (s.cols() + 3) & ~int64_t(3); }
+
+inline RowsChoice choose_rows(const RowsShape& s) {
+  const int64_t ntn = ceil_div(s.cols(), kRowsTileN), steps = std::max<int64_t>(1, ceil_div(s.length(), 64));
+  // By estimates of their times in units of 0.1 us: a step, and a tile's end.
+  static const int kBm[3] = {256, 128, 64}, kStep[3] = {12, 8, 6}, kEnd[3] = {60, 40, 30};
+  int64_t best = -1;
+  RowsChoice c{};
+  for (int i = 0; i < (s.pass == Pass::kWeight ? 2 : 3); ++i) {
+    for (int slices = 1; slices <= kMaxSlices && (slices == 1 || slices * 4 <= steps); slices *= 2) {
+      const int64_t tiles = s.row_tiles(kBm[i]) * ntn;
+      if (slices > 1 && tiles * slices > 2 * kCus) break;
+      const int64_t join = slices == 1 ? 0 : 50 + join_rows(s) * join_ld(s) * 4 * (slices + 1) / 400000;
+      const int64_t cost = ceil_div(tiles * slices, kCus) * (ceil_div(steps, slices) * kStep[i] + kEnd[i]) + join;
+      if (best < 0 || cost < best) {
+        best = cost;
+        c.bm = kBm[i];
+        c.slices = slices;
+      }
+    }
+  }
+  c.join = c.slices > 1 || (s.out_size == 4 && !s.pieces);
+  c.wide = c.join || s.pieces;
+  c.tiles = s.row_tiles_max(c.bm) * ntn * c.slices;
+  return c;
+}
+
+}  // namespace rows
+}  // namespace mxmoe

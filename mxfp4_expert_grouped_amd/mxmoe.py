@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_PKG, "libmxmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
 MOE_SRC_BF16, MOE_SRC_FP32, MOE_SRC_FP16 = 0, 1, 2
 MOE_ID_INT32, MOE_ID_INT64 = 0, 1
+MOE_ROWS_FORWARD, MOE_ROWS_INPUT, MOE_ROWS_WEIGHT = 0, 1, 2
 
 EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_quantize_act",
             "moe_forward", "moe_forward_noalloc", "moe_profile_begin", "moe_profile_end", "moe_packed_scale_bytes",
@@ -25,6 +26,7 @@ EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_quantize
             "moe_quantize_mx4", "moe_dequantize_mx4", "moe_linear_mx4",
             "moe_sort_tokens_workspace_bytes", "moe_sort_tokens", "moe_dispatch_rows",
             "moe_combine_rows", "moe_combine_rows_backward",
+            "moe_linear_rows_workspace_bytes", "moe_linear_rows", "moe_linear_rows_dx", "moe_linear_rows_dw",
             "moe_status_string", "moe_last_error")
 STAGES = ("router", "topk", "permute", "gate_up", "down", "combine")
 
@@ -143,6 +145,16 @@ def load_library(path: str = LIB_PATH):
                                               c_int64, c_void_p, c_void_p, c_int64, c_int32, c_void_p,
                                               c_void_p, c_int64, c_void_p, c_void_p]
     lib.moe_combine_rows_backward.restype = c_int
+    lib.moe_linear_rows_workspace_bytes.argtypes = [c_int, c_int, c_int64, c_int64, c_int64, c_int32, c_int32,
+                                                    c_int64, c_int64, c_int, c_int64, POINTER(c_size_t)]
+    lib.moe_linear_rows_workspace_bytes.restype = c_int
+    for fn in (lib.moe_linear_rows, lib.moe_linear_rows_dx):
+        fn.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_int64, c_void_p,
+                       c_int64, c_void_p, c_size_t, c_void_p]
+        fn.restype = c_int
+    lib.moe_linear_rows_dw.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_int32, c_void_p,
+                                       c_int64, c_int64, c_void_p, c_int, c_void_p, c_size_t, c_void_p]
+    lib.moe_linear_rows_dw.restype = c_int
     lib.moe_status_string.argtypes = [c_int]
     lib.moe_status_string.restype = c_char_p
     lib.moe_last_error.argtypes = []
@@ -293,3 +305,32 @@ def moe_combine_rows_backward(dy: int, rows: Optional[int], dtype: int, rows_cap
     _check(load_library().moe_combine_rows_backward(dy, rows, dtype, rows_cap, d, ld_dy, ld_rows, token_row,
                                                     w, num_tokens, top_k, num_rows, drows, ld_drows, dw,
                                                     stream))
+
+
+def moe_linear_rows_workspace_bytes(rows_pass: int, dtype: int, rows: int, ld_a: int, ld_x: int, mats: int, grouped: int,
+                                    n: int, k: int, out_dtype: int, ld_out: int) -> int:
+    out = c_size_t()
+    _check(load_library().moe_linear_rows_workspace_bytes(rows_pass, dtype, rows, ld_a, ld_x, mats, grouped, n, k,
+                                                          out_dtype, ld_out, ctypes.byref(out)))
+    return out.value
+
+
+def moe_linear_rows(x: int, dtype: int, rows: int, ld_x: int, w: int, mats: int, offsets: Optional[int], n: int, k: int,
+                    y: int, ld_y: int, workspace: Optional[int], workspace_bytes: int,
+                    stream: Optional[int] = None) -> None:
+    _check(load_library().moe_linear_rows(x, dtype, rows, ld_x, w, mats, offsets, n, k, y, ld_y, workspace,
+                                          workspace_bytes, stream))
+
+
+def moe_linear_rows_dx(dy: int, dtype: int, rows: int, ld_dy: int, w: int, mats: int, offsets: Optional[int], n: int,
+                       k: int, dx: int, ld_dx: int, workspace: Optional[int], workspace_bytes: int,
+                       stream: Optional[int] = None) -> None:
+    _check(load_library().moe_linear_rows_dx(dy, dtype, rows, ld_dy, w, mats, offsets, n, k, dx, ld_dx, workspace,
+                                             workspace_bytes, stream))
+
+
+def moe_linear_rows_dw(dy: int, dtype: int, rows: int, ld_dy: int, x: int, ld_x: int, mats: int, offsets: Optional[int],
+                       n: int, k: int, dw: int, dw_dtype: int, workspace: Optional[int], workspace_bytes: int,
+                       stream: Optional[int] = None) -> None:
+    _check(load_library().moe_linear_rows_dw(dy, dtype, rows, ld_dy, x, ld_x, mats, offsets, n, k, dw, dw_dtype,
+                                             workspace, workspace_bytes, stream))

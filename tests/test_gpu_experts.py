@@ -1,0 +1,106 @@
+"""16-bit products of rows sorted by expert and their gradients on the GPU,
+against float64.
+
+How far a result may be off: its rounding, half a step of its type, and the
+fp32 sum, whose error for L products is at most about L u times the sum of
+their magnitudes; u is taken as 2^-23, a whole step, since how the matrix
+cores round inside a sum is not documented.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mxfp4_expert_grouped_amd import mxmoe
+    mxmoe.load_library()
+    torch.cuda.set_device(0)
+    yield
+
+
+@pytest.fixture(scope="module")
+def X():
+    from mxfp4_expert_grouped_amd import experts
+    return experts
+
+
+def near(got, ref, mag, length):
+    """got (rounded to its type) against ref, a sum of `length` products whose magnitudes sum to mag (float64)"""
+    assert got.shape == ref.shape
+    step = torch.finfo(got.dtype).eps / 2
+    tiny = torch.finfo(got.dtype).smallest_normal * step  # half a step of the subnormal numbers
+    err = (got.double() - ref).abs()
+    tol = step * ref.abs() + tiny + (1 + step) * length * 2.0 ** -23 * mag
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, worst by {float((err / tol.clamp(min=1e-300)).max()):.3g} of what is allowed, first at {bad.nonzero()[0].tolist()}"
+
+
+def ragged(rows, mats, kind, seed):
+    """offsets [mats + 1] as a list"""
+    rng = np.random.default_rng(seed)
+    if kind == "even":
+        cuts = np.linspace(0, rows, mats + 1).round()
+    elif kind == "ragged":     # matrices without rows among them, all rows covered
+        cuts = np.sort(rng.integers(0, rows + 1, mats + 1))
+        cuts[0], cuts[-1] = 0, rows
+    elif kind == "uncovered":  # rows of no matrix in front and behind
+        cuts = np.sort(rng.integers(rows // 5, rows - rows // 4 + 1, mats + 1))
+    elif kind == "one":        # everything to one in the middle
+        cuts = np.where(np.arange(mats + 1) > mats // 2, rows, 0)
+    elif kind == "none":
+        cuts = np.full(mats + 1, rows // 2)
+    return [int(c) for c in cuts]
+
+
+def data(rows, mats, n, k, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(DT[dtype])  # noqa: E731
+    return rnd(rows, k), rnd(max(mats, 1), n, k), rnd(rows, n)
+
+
+def check_all(X, x, w, dy, offsets, dw_dtype=None):
+    """the product and both gradients by the functions without autograd"""
+    rows, (mats, n, k) = x.shape[0], w.shape
+    grouped = offsets is not None
+    cuts = offsets if grouped else [0, rows]
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda") if grouped else None
+    we = w if grouped else w[0]
+    y, dx, dw = X.linear(x, we, off), X.linear_dx(dy, we, off), X.linear_dw(dy, x, off, dtype=dw_dtype)
+    zero = lambda *s: torch.zeros(s, dtype=torch.float64, device="cuda")  # noqa: E731
+    ry, my, rdx, mdx, rdw, mdw = zero(rows, n), zero(rows, n), zero(rows, k), zero(rows, k), zero(mats, n, k), zero(mats, n, k)
+    for e in range(mats):
+        s = slice(cuts[e], cuts[e + 1])
+        xe, ye, wd = x[s].double(), dy[s].double(), w[e].double()
+        ry[s], my[s] = xe @ wd.T, xe.abs() @ wd.abs().T
+        rdx[s], mdx[s] = ye @ wd, ye.abs() @ wd.abs()
+        rdw[e], mdw[e] = ye.T @ xe, ye.abs().T @ xe.abs()
+    near(y, ry, my, k)
+    near(dx, rdx, mdx, n)
+    near(dw, rdw if grouped else rdw[0], mdw if grouped else mdw[0], max(b - a for a, b in zip(cuts, cuts[1:])))
+    return y, dx, dw
+
+
+# rows, matrices (0: one without offsets), n, k
+SIZES = [(1, 0, 1, 1), (1, 0, 8, 8), (3, 0, 64, 64), (64, 0, 256, 64), (65, 0, 257, 65), (300, 0, 512, 320), (1000, 0, 24, 4096),
+         (257, 1, 256, 256), (40, 3, 72, 136), (500, 7, 264, 200), (999, 13, 131, 77), (2000, 40, 520, 72), (128, 300, 32, 40),
+         (5000, 3, 128, 128), (700, 2, 1000, 1032), (77, 5, 2, 3), (4096, 9, 384, 640)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,mats,n,k", SIZES)
+def test_products_and_gradients(X, rows, mats, n, k, dtype):
+    x, w, dy = data(rows, mats, n, k, dtype, rows + n)
+    if not mats:
+        check_all(X, x, w, dy, None)
+        check_all(X, x, w, dy, None, torch.float32)
+        return
+    for kind in ("even", "ragged", "uncovered", "one", "none"):
+        check_all(X, x, w, dy, ragged(rows, mats, kind, k), torch.float32 if kind == "even" else None)
