@@ -416,7 +416,10 @@ typedef enum { MOE_ROWS_FORWARD = 0, MOE_ROWS_INPUT = 1, MOE_ROWS_WEIGHT = 2 } m
  * bytes: widths and strides that are multiples of 8 are the fast case.  Its
  * arguments are the call's own: ld_a the stride of x (forward) or dy, ld_x
  * that of x for dw (else 0), grouped whether offsets are given, out_dt the
- * result's type, ld_out its stride (dw: k). */
+ * result's type, ld_out its stride (dw: k).
+ * x of dw may come in 8 bits instead (x NULL, ld_x 0): x_codes [rows][k] and
+ * x_scales [rows][ceil(k/32)] as moe_quantize_mx8 makes them, taken by their
+ * values in dt; the workspace then holds those. */
 moe_status moe_linear_rows_workspace_bytes(moe_rows_pass pass, moe_src_dtype dt, int64_t rows,
                                            int64_t ld_a, int64_t ld_x, int32_t mats,
                                            int32_t grouped, int64_t n, int64_t k,
@@ -431,9 +434,49 @@ moe_status moe_linear_rows_dx(const void *dy, moe_src_dtype dt, int64_t rows, in
                               int64_t k, void *dx, int64_t ld_dx, void *workspace,
                               size_t workspace_bytes, void *stream);
 moe_status moe_linear_rows_dw(const void *dy, moe_src_dtype dt, int64_t rows, int64_t ld_dy,
-                              const void *x, int64_t ld_x, int32_t mats, const int32_t *offsets,
+                              const void *x, int64_t ld_x, const uint8_t *x_codes,
+                              const uint8_t *x_scales, int32_t mats, const int32_t *offsets,
                               int64_t n, int64_t k, void *dw, moe_src_dtype dw_dt,
                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Activations kept in 8 bits until the backward pass.  MXFP8 of the rows of a
+ * bf16, fp16 or fp32 matrix of any width: per row and per 32 consecutive
+ * columns (fewer at its end), e = clamp(floor(log2 amax) - 8, -127, 127)
+ * (amax == 0 -> -127), codes = E4M3 round-to-nearest-even of v / 2^e with
+ * saturation to +-448 (sign kept on zero), scale byte = e + 127: a kept value
+ * is off by at most 2^-4 of itself, or by 2^(e-10) where that is more (a value
+ * that saturates by up to an eighth of itself).  A block with an infinity or a
+ * NaN gets the scale 255 (NaN) and zero codes.
+ * src [rows][ld_src]; codes [rows][cols], scales [rows][ceil(cols/32)].
+ * ld_src >= cols, rows <= 2^40, cols <= 2^28; src aligned to its element.
+ * Rows on 16 bytes and codes' rows on 8 are the fast case. */
+moe_status moe_quantize_mx8(const void *src, moe_src_dtype dt, int64_t rows, int64_t cols,
+                            int64_t ld_src, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values of moe_quantize_mx8's codes, code * 2^(scale - 127) rounded to
+ * nearest even to dt (exact in bf16 and fp32 but for bf16's subnormal
+ * numbers); a block with scale 255 is NaN.  dst [rows][ld_dst]. */
+moe_status moe_dequantize_mx8(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                              int64_t cols, void *dst, moe_src_dtype dt, int64_t ld_dst,
+                              void *stream);
+
+/* The gated activation between an expert's projections, row by row:
+ *   a = silu(g) u,  g = h[0 .. d_ff), u = h[d_ff .. 2 d_ff), silu(g) = g / (1 + exp(-g))
+ * in fp32, rounded once to dt (bf16, fp16 or fp32).  h [rows][ld_h], a
+ * [rows][ld_a].  codes [rows][2 d_ff] and scales [rows][2 ceil(d_ff/32)] (both
+ * or neither): g and u in 8 bits as moe_quantize_mx8 has them, each half with
+ * blocks of its own, g's first.
+ * backward, from da [rows][ld_da] and from h or (h NULL) its codes:
+ *   dh = (da u s (1 + g (1 - s)), da g s),  s = 1 / (1 + exp(-g))
+ *   a    as above, of the same g and u (NULL: skipped)
+ * rows <= 2^40, d_ff <= 2^28; buffers aligned to their elements.  Rows and
+ * halves on 16 bytes (codes: 8) are the fast case. */
+moe_status moe_swiglu(const void *h, moe_src_dtype dt, int64_t rows, int64_t d_ff, int64_t ld_h,
+                      void *a, int64_t ld_a, uint8_t *codes, uint8_t *scales, void *stream);
+moe_status moe_swiglu_backward(const void *da, moe_src_dtype dt, int64_t rows, int64_t d_ff,
+                               int64_t ld_da, const void *h, int64_t ld_h, const uint8_t *codes,
+                               const uint8_t *scales, void *dh, int64_t ld_dh, void *a,
+                               int64_t ld_a, void *stream);
 
 /* Stages of moe_forward, for per-stage timing. */
 typedef enum {

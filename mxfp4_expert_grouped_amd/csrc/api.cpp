@@ -861,12 +861,14 @@ struct RowsCall {
   rows::RowsChoice c;
   // operands that are laid out in the workspace first, rows on 16 bytes
   bool pad_a, pad_b;
+  bool codes;                        // x of the weights' gradient comes in 8 bits (and is laid out so)
   int64_t ld_a, ld_b;                // row strides of the operands as the kernels read them
   size_t off_a, off_b, off_part, total;
 };
 
 // Checks of what does not depend on pointers; -> the call's layout.  a: x or
-// dy, ld_a apart; for the weights' gradient ld_x is the stride of x.
+// dy, ld_a apart; for the weights' gradient ld_x is the stride of x, 0 where
+// it comes in 8 bits.
 moe_status plan_rows(moe_rows_pass pass, moe_src_dtype dt, int64_t nrows, int64_t ld_a, int64_t ld_x, int32_t mats, bool grouped,
                      int64_t n, int64_t k, moe_src_dtype out_dt, int64_t ld_out, RowsCall& p) {
   if (pass != MOE_ROWS_FORWARD && pass != MOE_ROWS_INPUT && pass != MOE_ROWS_WEIGHT) return fail(MOE_ERR_INVALID_ARG, "bad pass");
@@ -878,7 +880,8 @@ moe_status plan_rows(moe_rows_pass pass, moe_src_dtype dt, int64_t nrows, int64_
   if (mats > rows::kMaxRowMats || n > (1 << 20) || k > (1 << 20) || nrows > (1 << 25))
     return fail(MOE_ERR_UNSUPPORTED, "more than 1024 matrices, 2^20 columns or 2^25 rows");
   const int64_t wa = pass == MOE_ROWS_FORWARD ? k : n, wo = pass == MOE_ROWS_FORWARD ? n : k;
-  if (ld_a < wa || (pass == MOE_ROWS_WEIGHT && ld_x < k) || (pass != MOE_ROWS_WEIGHT && ld_out < wo))
+  p.codes = pass == MOE_ROWS_WEIGHT && ld_x == 0;
+  if (ld_a < wa || (pass == MOE_ROWS_WEIGHT && !p.codes && ld_x < k) || (pass != MOE_ROWS_WEIGHT && ld_out < wo))
     return fail(MOE_ERR_INVALID_ARG, "row stride below the row's width");
   if (ld_a > (1 << 21) || ld_x > (1 << 21) || ld_out > (1 << 21)) return fail(MOE_ERR_UNSUPPORTED, "row stride above 2^21");
   const int64_t tn = rows::ceil_div(wo, rows::kRowsTileN);
@@ -890,7 +893,7 @@ moe_status plan_rows(moe_rows_pass pass, moe_src_dtype dt, int64_t nrows, int64_
   p.c = rows::choose_rows(p.s);
   // rows of whole pieces of 16 bytes are read where they are
   p.pad_a = wa % 8 || ld_a % 8;
-  p.pad_b = pass == MOE_ROWS_WEIGHT ? (k % 8 || ld_x % 8) : k % 8 != 0;
+  p.pad_b = p.codes || (pass == MOE_ROWS_WEIGHT ? (k % 8 || ld_x % 8) : k % 8 != 0);
   p.ld_a = p.pad_a ? rows::round8(wa) : ld_a;
   p.ld_b = p.pad_b ? rows::round8(k) : pass == MOE_ROWS_WEIGHT ? ld_x : k;
   size_t at = 0;
@@ -906,12 +909,12 @@ moe_status plan_rows(moe_rows_pass pass, moe_src_dtype dt, int64_t nrows, int64_
   return MOE_OK;
 }
 
-// Runs the product: a as above, b is w or x.
-moe_status run_rows(RowsCall& p, moe_src_dtype dt, const void* a, int64_t ld_a, const void* b, int64_t ld_b, const int32_t* offsets,
-                    void* out, moe_src_dtype out_dt, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
+// Runs the product: a as above, b is w or x (its codes, with x_scales).
+moe_status run_rows(RowsCall& p, moe_src_dtype dt, const void* a, int64_t ld_a, const void* b, int64_t ld_b, const uint8_t* x_scales,
+                    const int32_t* offsets, void* out, moe_src_dtype out_dt, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
   const rows::RowsShape& s = p.s;
   const bool weight = s.pass == Pass::kWeight;
-  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, s.out_size) || !aligned(offsets, 4))
+  if (!aligned(a, 16) || (!p.codes && !aligned(b, 16)) || !aligned(out, s.out_size) || !aligned(offsets, 4))
     return fail(MOE_ERR_INVALID_ARG, "misaligned buffer (operands: 16 bytes; offsets: 4; the result: its element, 16 bytes as fp32)");
   if (s.out_size == 4 && !aligned(out, 16)) return fail(MOE_ERR_INVALID_ARG, "an fp32 result needs 16-byte alignment");
   if (p.total && (!workspace || workspace_bytes < p.total))
@@ -933,7 +936,8 @@ moe_status run_rows(RowsCall& p, moe_src_dtype dt, const void* a, int64_t ld_a, 
     a = ws + p.off_a;
   }
   if (p.pad_b && e == hipSuccess) {
-    e = rows::launch_pad_rows(b, weight ? s.rows : s.mats * s.n, s.k, ld_b, ws + p.off_b, p.ld_b, hs);
+    e = p.codes ? launch_dequantize_mx8(static_cast<const uint8_t*>(b), x_scales, s.rows, s.k, ws + p.off_b, t, p.ld_b, p.ld_b, hs)
+                : rows::launch_pad_rows(b, weight ? s.rows : s.mats * s.n, s.k, ld_b, ws + p.off_b, p.ld_b, hs);
     b = ws + p.off_b;
   }
   if (e != hipSuccess) return launched(e);
@@ -990,7 +994,7 @@ moe_status moe_linear_rows(const void* x, moe_src_dtype dt, int64_t num_rows, in
   moe_status s = plan_rows(MOE_ROWS_FORWARD, dt, num_rows, ld_x, 0, mats, offsets != nullptr, n, k, dt, ld_y, p);
   if (s != MOE_OK || num_rows == 0 || n == 0) return s;
   if (!y || (k > 0 && (!x || !w))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
-  return run_rows(p, dt, x, ld_x, w, k, offsets, y, dt, ld_y, workspace, workspace_bytes, stream);
+  return run_rows(p, dt, x, ld_x, w, k, nullptr, offsets, y, dt, ld_y, workspace, workspace_bytes, stream);
 }
 
 moe_status moe_linear_rows_dx(const void* dy, moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, const void* w, int32_t mats,
@@ -1000,17 +1004,118 @@ moe_status moe_linear_rows_dx(const void* dy, moe_src_dtype dt, int64_t num_rows
   moe_status s = plan_rows(MOE_ROWS_INPUT, dt, num_rows, ld_dy, 0, mats, offsets != nullptr, n, k, dt, ld_dx, p);
   if (s != MOE_OK || num_rows == 0 || k == 0) return s;
   if (!dx || (n > 0 && (!dy || !w))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
-  return run_rows(p, dt, dy, ld_dy, w, k, offsets, dx, dt, ld_dx, workspace, workspace_bytes, stream);
+  return run_rows(p, dt, dy, ld_dy, w, k, nullptr, offsets, dx, dt, ld_dx, workspace, workspace_bytes, stream);
 }
 
 moe_status moe_linear_rows_dw(const void* dy, moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, const void* x, int64_t ld_x,
-                              int32_t mats, const int32_t* offsets, int64_t n, int64_t k, void* dw, moe_src_dtype dw_dt,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              const uint8_t* x_codes, const uint8_t* x_scales, int32_t mats, const int32_t* offsets, int64_t n,
+                              int64_t k, void* dw, moe_src_dtype dw_dt, void* workspace, size_t workspace_bytes, void* stream) {
+  if (x && (x_codes || x_scales)) return fail(MOE_ERR_INVALID_ARG, "x comes in its own type or in 8 bits, not both");
+  if (!x_codes != !x_scales) return fail(MOE_ERR_INVALID_ARG, "codes without scales, or scales without codes");
+  if ((x_codes && ld_x != 0) || (x && ld_x == 0 && k > 0)) return fail(MOE_ERR_INVALID_ARG, "ld_x is 0 for x in 8 bits, and only then");
   RowsCall p;
   moe_status s = plan_rows(MOE_ROWS_WEIGHT, dt, num_rows, ld_dy, ld_x, mats, offsets != nullptr, n, k, dw_dt, k, p);
   if (s != MOE_OK || n == 0 || k == 0) return s;
-  if (!dw || (num_rows > 0 && (!dy || !x))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
-  return run_rows(p, dt, dy, ld_dy, x, ld_x, offsets, dw, dw_dt, k, workspace, workspace_bytes, stream);
+  if (!dw || (num_rows > 0 && (!dy || !(x || x_codes)))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  return run_rows(p, dt, dy, ld_dy, x_codes ? x_codes : x, ld_x, x_scales, offsets, dw, dw_dt, k, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Activations in 8 bits, the gated activation
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMostRows = int64_t(1) << 40, kMostCols = int64_t(1) << 28;
+
+moe_status check_mx8(const void* plain, moe_src_dtype dt, int64_t rows, int64_t cols, int64_t ld, const uint8_t* codes,
+                     const uint8_t* scales, RowType& t) {
+  int64_t sz;
+  if (!row_type(dt, t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "negative size");
+  if (rows > kMostRows || cols > kMostCols || ld > kMostRows)
+    return fail(MOE_ERR_UNSUPPORTED, "rows above 2^40, cols above 2^28 or row stride above 2^40");
+  if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "row stride < cols");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!plain || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(plain, sz)) return fail(MOE_ERR_INVALID_ARG, "the plain matrix needs the alignment of its elements");
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_mx8(const void* src, moe_src_dtype dt, int64_t rows, int64_t cols, int64_t ld_src, uint8_t* codes,
+                            uint8_t* scales, void* stream) {
+  RowType t;
+  moe_status s = check_mx8(src, dt, rows, cols, ld_src, codes, scales, t);
+  if (s != MOE_OK || rows == 0 || cols == 0) return s;
+  s = check_device();
+  if (s != MOE_OK) return s;
+  return launched(launch_quantize_mx8(src, t, rows, cols, ld_src, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_dequantize_mx8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* dst,
+                              moe_src_dtype dt, int64_t ld_dst, void* stream) {
+  RowType t;
+  moe_status s = check_mx8(dst, dt, rows, cols, ld_dst, codes, scales, t);
+  if (s != MOE_OK || rows == 0 || cols == 0) return s;
+  s = check_device();
+  if (s != MOE_OK) return s;
+  return launched(launch_dequantize_mx8(codes, scales, rows, cols, dst, t, ld_dst, cols, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_swiglu(const void* h, moe_src_dtype dt, int64_t rows, int64_t d_ff, int64_t ld_h, void* a, int64_t ld_a,
+                      uint8_t* codes, uint8_t* scales, void* stream) {
+  RowType t;
+  int64_t sz;
+  if (!row_type(dt, t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  if (rows < 0 || d_ff < 0) return fail(MOE_ERR_INVALID_ARG, "negative size");
+  if (rows > kMostRows || d_ff > kMostCols || ld_h > kMostRows || ld_a > kMostRows)
+    return fail(MOE_ERR_UNSUPPORTED, "rows above 2^40, d_ff above 2^28 or row stride above 2^40");
+  if (ld_h < 2 * d_ff || ld_a < d_ff) return fail(MOE_ERR_INVALID_ARG, "row stride below the row's width");
+  if (!codes != !scales) return fail(MOE_ERR_INVALID_ARG, "codes without scales, or scales without codes");
+  if (rows == 0 || d_ff == 0) return MOE_OK;
+  if (!h || !a) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(h, sz) || !aligned(a, sz)) return fail(MOE_ERR_INVALID_ARG, "misaligned buffer");
+  moe_status s = check_device();
+  if (s != MOE_OK) return s;
+  SwigluArgs g{};
+  g.rows = rows; g.f = d_ff;
+  g.h = h; g.ld_h = ld_h;
+  g.a = a; g.ld_a = ld_a;
+  g.codes = codes; g.scales = scales;
+  return launched(launch_swiglu(g, t, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_swiglu_backward(const void* da, moe_src_dtype dt, int64_t rows, int64_t d_ff, int64_t ld_da, const void* h,
+                               int64_t ld_h, const uint8_t* codes, const uint8_t* scales, void* dh, int64_t ld_dh, void* a,
+                               int64_t ld_a, void* stream) {
+  RowType t;
+  int64_t sz;
+  if (!row_type(dt, t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  if (rows < 0 || d_ff < 0) return fail(MOE_ERR_INVALID_ARG, "negative size");
+  if (rows > kMostRows || d_ff > kMostCols || ld_da > kMostRows || ld_h > kMostRows || ld_dh > kMostRows || ld_a > kMostRows)
+    return fail(MOE_ERR_UNSUPPORTED, "rows above 2^40, d_ff above 2^28 or row stride above 2^40");
+  if (ld_da < d_ff || ld_dh < 2 * d_ff || (h && ld_h < 2 * d_ff) || (a && ld_a < d_ff))
+    return fail(MOE_ERR_INVALID_ARG, "row stride below the row's width");
+  if (!codes != !scales) return fail(MOE_ERR_INVALID_ARG, "codes without scales, or scales without codes");
+  if (h && codes) return fail(MOE_ERR_INVALID_ARG, "h comes in its own type or in 8 bits, not both");
+  if (rows == 0 || d_ff == 0) return MOE_OK;
+  if (!da || !dh || !(h || codes)) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(da, sz) || !aligned(h, sz) || !aligned(dh, sz) || !aligned(a, sz)) return fail(MOE_ERR_INVALID_ARG, "misaligned buffer");
+  moe_status s = check_device();
+  if (s != MOE_OK) return s;
+  SwigluArgs g{};
+  g.rows = rows; g.f = d_ff;
+  g.h = h; g.ld_h = ld_h;
+  g.a = a; g.ld_a = ld_a;
+  g.codes = const_cast<uint8_t*>(codes); g.scales = const_cast<uint8_t*>(scales);
+  g.da = da; g.ld_da = ld_da;
+  g.dh = dh; g.ld_dh = ld_dh;
+  return launched(launch_swiglu(g, t, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

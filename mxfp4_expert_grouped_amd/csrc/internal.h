@@ -258,6 +258,28 @@ hipError_t launch_join(const float* part, int slices, int64_t rows, int64_t cols
                        void* out, RowType out_t, int64_t ld_out, hipStream_t st);
 }  // namespace rows
 
+// ---- activations in 8 bits, the gated activation
+hipError_t launch_quantize_mx8(const void* src, RowType dt, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                               uint8_t* scales, hipStream_t st);
+// pad (cols <= pad < cols + 8) columns of dst are written, zeros from cols on
+hipError_t launch_dequantize_mx8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* dst,
+                                 RowType dt, int64_t ld, int64_t pad, hipStream_t st);
+// forward (dh null): a from h, and codes of h where they are given; backward:
+// dh, and a where it is given, from da and h, or from its codes
+struct SwigluArgs {
+  int64_t rows, f;
+  const void* h;
+  int64_t ld_h;
+  void* a;
+  int64_t ld_a;
+  uint8_t *codes, *scales;
+  const void* da;
+  int64_t ld_da;
+  void* dh;
+  int64_t ld_dh;
+};
+hipError_t launch_swiglu(const SwigluArgs& s, RowType dt, hipStream_t st);
+
 // bytes of one packed scale matrix [rows/16][ceil(k/512)][64][4]
 __host__ __device__ inline int64_t packed_scale_bytes(int64_t rows, int64_t k) { return rows * (k / 32); }
 

@@ -7,6 +7,7 @@
 
 #include "internal.h"
 #include "row_types.h"
+#include "rows_device.h"
 
 namespace mxmoe {
 namespace rows {
@@ -42,16 +43,14 @@ template <typename T>
 __global__ void __launch_bounds__(kAuxThreads) k_join(const float* __restrict__ part, int slices, int64_t slice, int64_t quads,
                                                       int per_row, int cols, const int* __restrict__ offsets, int mats, int64_t rows,
                                                       T* __restrict__ out, int64_t ld_out) {
-  int64_t lo = 0, hi = rows;
-  if (offsets) {  // rows of no matrix have no sums
-    lo = min(max(int64_t(offsets[0]), int64_t(0)), rows);
-    hi = max(lo, min(max(int64_t(offsets[mats]), int64_t(0)), rows));
-  }
+  __shared__ int part_rows[2 * kAuxThreads / 64];
+  int lo = 0, hi = 0;
+  if (offsets) covered_rows<kAuxThreads>(offsets, mats, static_cast<int>(rows), lo, hi, part_rows);  // (others have no sums)
   for (int64_t p = int64_t(blockIdx.x) * kAuxThreads + threadIdx.x; p < quads; p += int64_t(gridDim.x) * kAuxThreads) {
     const int64_t row = quads < (int64_t(1) << 31) ? static_cast<uint32_t>(p) / static_cast<uint32_t>(per_row) : p / per_row;
     const int col = 4 * static_cast<int>(p - row * per_row);
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (row >= lo && row < hi) {
+    if (!offsets || (row >= lo && row < hi)) {
       for (int i = 0; i < slices; ++i) {
         const f32x4 v = *reinterpret_cast<const f32x4*>(part + i * slice + 4 * p);
         s[0] += v[0]; s[1] += v[1]; s[2] += v[2]; s[3] += v[3];

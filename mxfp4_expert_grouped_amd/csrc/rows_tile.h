@@ -17,6 +17,7 @@
 #include "internal.h"
 #include "rows_choice.h"
 #include "row_types.h"
+#include "rows_device.h"
 
 namespace mxmoe {
 namespace rows {
@@ -39,19 +40,6 @@ __device__ __forceinline__ v16f mfma32(v8s b, v8s a, v16f c) {
   }
 }
 
-// Rows of matrix e: clamped into [0, rows] and never running backwards within
-// a matrix, so that no value of the offsets reaches outside a buffer.
-__device__ __forceinline__ void mat_rows(const RowsArgs& a, int e, int& lo, int& hi) {
-  const int rows = static_cast<int>(a.rows);
-  if (!a.offsets) {
-    lo = 0;
-    hi = rows;
-    return;
-  }
-  lo = min(max(a.offsets[e], 0), rows);
-  hi = max(lo, min(max(a.offsets[e + 1], 0), rows));
-}
-
 // prefix[e] = row tiles (of TM rows) of the matrices before e; one pass of the
 // whole workgroup (part: a word of LDS per wave).  Returns the number of tiles.
 template <int THREADS, int TM>
@@ -68,7 +56,7 @@ __device__ __forceinline__ int tile_prefix(const RowsArgs& a, int* prefix, int* 
   for (int i = 0; i < PER; ++i) {
     const int e = tid * PER + i;
     int lo = 0, hi = 0;
-    if (e < a.mats) mat_rows(a, e, lo, hi);
+    if (e < a.mats) mat_rows(a.offsets, e, static_cast<int>(a.rows), lo, hi);
     n[i] = (hi - lo + TM - 1) / TM;
     sum += n[i];
   }
@@ -271,9 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
     int lo = 0, hi = static_cast<int>(a.rows);
     if (a.offsets) {
       sload2(a.offsets + t.e, lo, hi);
-      const int rows = static_cast<int>(a.rows);
-      lo = min(max(lo, 0), rows);
-      hi = max(lo, min(max(hi, 0), rows));
+      clamp_rows(static_cast<int>(a.rows), lo, hi);
     }
     t.col0 = nt * kRowsTileN;
     if constexpr (PASS == Pass::kWeight) {
@@ -583,9 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   // ---- rows of no matrix are zero (of partial sums the joining kernel does it)
   if constexpr (PASS != Pass::kWeight) {
     if (!a.offsets || a.slices > 1) return;
-    const int rows = static_cast<int>(a.rows);
-    const int lo = min(max(a.offsets[0], 0), rows), hi = max(lo, min(max(a.offsets[a.mats], 0), rows));
-    const int none = lo + rows - hi;
+    __syncthreads();  // all waves are done with the LDS
+    int lo, hi;
+    covered_rows<kThreads>(a.offsets, a.mats, static_cast<int>(a.rows), lo, hi, reinterpret_cast<int*>(lds));
+    const int none = lo + static_cast<int>(a.rows) - hi;
     TO* c = static_cast<TO*>(a.c);
     for (int i = b; i < none; i += G) {
       TO* row = c + int64_t(i < lo ? i : i - lo + hi) * a.ld_c;

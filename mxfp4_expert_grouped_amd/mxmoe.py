@@ -27,6 +27,7 @@ EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_quantize
             "moe_sort_tokens_workspace_bytes", "moe_sort_tokens", "moe_dispatch_rows",
             "moe_combine_rows", "moe_combine_rows_backward",
             "moe_linear_rows_workspace_bytes", "moe_linear_rows", "moe_linear_rows_dx", "moe_linear_rows_dw",
+            "moe_quantize_mx8", "moe_dequantize_mx8", "moe_swiglu", "moe_swiglu_backward",
             "moe_status_string", "moe_last_error")
 STAGES = ("router", "topk", "permute", "gate_up", "down", "combine")
 
@@ -152,9 +153,20 @@ def load_library(path: str = LIB_PATH):
         fn.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_int64, c_void_p,
                        c_int64, c_void_p, c_size_t, c_void_p]
         fn.restype = c_int
-    lib.moe_linear_rows_dw.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_int32, c_void_p,
-                                       c_int64, c_int64, c_void_p, c_int, c_void_p, c_size_t, c_void_p]
+    lib.moe_linear_rows_dw.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                                       c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int, c_void_p, c_size_t,
+                                       c_void_p]
     lib.moe_linear_rows_dw.restype = c_int
+    lib.moe_quantize_mx8.argtypes = lib.moe_quantize_mx4.argtypes
+    lib.moe_quantize_mx8.restype = c_int
+    lib.moe_dequantize_mx8.argtypes = lib.moe_dequantize_mx4.argtypes
+    lib.moe_dequantize_mx8.restype = c_int
+    lib.moe_swiglu.argtypes = [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                               c_void_p]
+    lib.moe_swiglu.restype = c_int
+    lib.moe_swiglu_backward.argtypes = [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p,
+                                        c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
+    lib.moe_swiglu_backward.restype = c_int
     lib.moe_status_string.argtypes = [c_int]
     lib.moe_status_string.restype = c_char_p
     lib.moe_last_error.argtypes = []
@@ -329,8 +341,31 @@ def moe_linear_rows_dx(dy: int, dtype: int, rows: int, ld_dy: int, w: int, mats:
                                              workspace_bytes, stream))
 
 
-def moe_linear_rows_dw(dy: int, dtype: int, rows: int, ld_dy: int, x: int, ld_x: int, mats: int, offsets: Optional[int],
-                       n: int, k: int, dw: int, dw_dtype: int, workspace: Optional[int], workspace_bytes: int,
+def moe_linear_rows_dw(dy: int, dtype: int, rows: int, ld_dy: int, x: Optional[int], ld_x: int, x_codes: Optional[int],
+                       x_scales: Optional[int], mats: int, offsets: Optional[int], n: int, k: int, dw: int,
+                       dw_dtype: int, workspace: Optional[int], workspace_bytes: int,
                        stream: Optional[int] = None) -> None:
-    _check(load_library().moe_linear_rows_dw(dy, dtype, rows, ld_dy, x, ld_x, mats, offsets, n, k, dw, dw_dtype,
-                                             workspace, workspace_bytes, stream))
+    _check(load_library().moe_linear_rows_dw(dy, dtype, rows, ld_dy, x, ld_x, x_codes, x_scales, mats, offsets, n, k, dw,
+                                             dw_dtype, workspace, workspace_bytes, stream))
+
+
+def moe_quantize_mx8(src: int, src_dtype: int, rows: int, cols: int, ld_src: int, codes: int, scales: int,
+                     stream: Optional[int] = None) -> None:
+    _check(load_library().moe_quantize_mx8(src, src_dtype, rows, cols, ld_src, codes, scales, stream))
+
+
+def moe_dequantize_mx8(codes: int, scales: int, rows: int, cols: int, dst: int, dst_dtype: int, ld_dst: int,
+                       stream: Optional[int] = None) -> None:
+    _check(load_library().moe_dequantize_mx8(codes, scales, rows, cols, dst, dst_dtype, ld_dst, stream))
+
+
+def moe_swiglu(h: int, dtype: int, rows: int, d_ff: int, ld_h: int, a: int, ld_a: int, codes: Optional[int],
+               scales: Optional[int], stream: Optional[int] = None) -> None:
+    _check(load_library().moe_swiglu(h, dtype, rows, d_ff, ld_h, a, ld_a, codes, scales, stream))
+
+
+def moe_swiglu_backward(da: int, dtype: int, rows: int, d_ff: int, ld_da: int, h: Optional[int], ld_h: int,
+                        codes: Optional[int], scales: Optional[int], dh: int, ld_dh: int, a: Optional[int], ld_a: int,
+                        stream: Optional[int] = None) -> None:
+    _check(load_library().moe_swiglu_backward(da, dtype, rows, d_ff, ld_da, h, ld_h, codes, scales, dh, ld_dh, a, ld_a,
+                                              stream))

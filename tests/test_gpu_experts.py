@@ -104,3 +104,78 @@ def test_products_and_gradients(X, rows, mats, n, k, dtype):
         return
     for kind in ("even", "ragged", "uncovered", "one", "none"):
         check_all(X, x, w, dy, ragged(rows, mats, kind, k), torch.float32 if kind == "even" else None)
+
+
+@pytest.mark.parametrize("rows,mats,n,k,dtype", [(300, 5, 136, 256, "bf16"), (513, 0, 72, 100, "bf16"), (90, 4, 33, 31, "fp16"), (1, 1, 8, 5, "bf16"),
+                                                 (0, 3, 16, 40, "bf16")])
+def test_weights_gradient_from_rows_in_8_bits(X, rows, mats, n, k, dtype):
+    x, w, dy = data(rows, mats, n, k, dtype, 7)
+    kept = X.quantize_mx8(x)
+    values = X.dequantize_mx8(*kept, DT[dtype])
+    off = torch.tensor(ragged(rows, mats, "uncovered", 1), dtype=torch.int32, device="cuda") if mats else None
+    for out in (None, torch.float32):
+        assert torch.equal(X.linear_dw(dy, kept, off, dtype=out), X.linear_dw(dy, values, off, dtype=out))
+
+
+def test_rows_with_a_nan_scale_reach_their_columns_only(X):
+    x, _, dy = data(40, 2, 16, 70, "bf16", 9)
+    x[3, 33] = float("inf")  # in the first matrix
+    off = torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda")
+    dw = X.linear_dw(dy, X.quantize_mx8(x), off)
+    assert dw[0, :, 32:64].isnan().all() and not dw[0, :, :32].isnan().any() and not dw[0, :, 64:].isnan().any() and not dw[1].isnan().any()
+
+
+def test_rows_of_no_matrix_are_not_read(X):
+    # what lies there, NaN included, reaches nothing
+    x, w, dy = data(200, 3, 64, 72, "bf16", 2)
+    off = torch.tensor([30, 90, 90, 150], dtype=torch.int32, device="cuda")
+    want = X.linear(x, w, off), X.linear_dx(dy, w, off), X.linear_dw(dy, x, off)
+    for t in (x, dy):
+        t[:30], t[150:] = float("nan"), float("inf")
+    got = X.linear(x, w, off), X.linear_dx(dy, w, off), X.linear_dw(dy, x, off)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert not want[0][:30].any() and not want[0][150:].any() and not want[1][:30].any() and not want[2][1].any()
+
+
+def test_views(X):
+    x, w, dy = data(120, 3, 128, 96, "bf16", 5)
+    off = torch.tensor([0, 50, 70, 120], dtype=torch.int32, device="cuda")
+    want = X.linear(x, w, off), X.linear_dx(dy, w, off), X.linear_dw(dy, x, off)
+    big = lambda t, left, right: torch.nn.functional.pad(t, (left, right), value=float("nan"))[:, left:left + t.shape[1]]  # noqa: E731
+    for xv, wv, dv, ov in ((big(x, 8, 8), w, big(dy, 0, 8), off), (big(x, 3, 2), w, big(dy, 1, 1), off),
+                           (x.t().contiguous().t(), w.transpose(1, 2).contiguous().transpose(1, 2), dy.t().contiguous().t(), off),
+                           (x, w, dy, torch.stack((off, off), 1)[:, 0]), (x.repeat_interleave(2, 0)[::2], w, dy.repeat_interleave(2, 0)[1::2], off)):
+        got = X.linear(xv, wv, ov), X.linear_dx(dv, wv, ov), X.linear_dw(dv, xv, ov)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_broadcast_gradient(X):
+    x, w, _ = data(33, 0, 40, 56, "bf16", 6)
+    xl, wl = x.requires_grad_(), w[0].requires_grad_()
+    gx, gw = torch.autograd.grad(X.linear(xl, wl).sum(), (xl, wl))
+    one = torch.ones(33, 40, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(gx, X.linear_dx(one, wl.detach())) and torch.equal(gw, X.linear_dw(one, xl.detach()))
+
+
+def test_sizes_of_zero(X):
+    e = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert X.linear(e(0, 8), e(5, 8)).shape == (0, 5)
+    assert X.linear(e(4, 8), e(0, 8)).shape == (4, 0)
+    assert torch.equal(X.linear(e(4, 0), e(5, 0)), e(4, 5) * 0)
+    assert torch.equal(X.linear(e(4, 8), e(3, 5, 8), off), e(4, 5) * 0)
+    assert torch.equal(X.linear_dx(e(4, 0), e(0, 8)), e(4, 8) * 0)
+    for x in (e(0, 8), X.quantize_mx8(e(0, 8))):
+        assert torch.equal(X.linear_dw(e(0, 5), x), e(5, 8) * 0)
+        assert torch.equal(X.linear_dw(e(0, 5), x, off), e(3, 5, 8) * 0)
+    assert X.linear_dw(e(3, 0), e(3, 8)).shape == (0, 8) and X.linear_dw(e(3, 5), e(3, 0)).shape == (5, 0)
+
+
+def test_offsets_out_of_range_stay_inside(X):
+    # values that no sort gives: taken as the nearer end, never outside a buffer
+    x, w, dy = data(50, 3, 24, 32, "bf16", 8)
+    wild = torch.tensor([-7, 10, 1 << 30, -5], dtype=torch.int32, device="cuda")
+    tame = torch.tensor([0, 10, 50, 50], dtype=torch.int32, device="cuda")
+    y, t = X.linear(x, w, wild), X.linear(x, w, tame)
+    assert torch.equal(y, t)
+    assert torch.equal(X.linear_dw(dy, x, wild)[:2], X.linear_dw(dy, x, tame)[:2])
