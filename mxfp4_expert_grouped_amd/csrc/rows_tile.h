@@ -201,7 +201,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   using P = Shape<BM, sizeof(TO)>;
   using SA = Side<TA, BM>;
   using SB = Side<TB, kRowsTileN>;
-  constexpr int S = P::S, MI = P::MI, NI = P::NI, NM = MI * NI;
+  constexpr int S = P::S, MI = P::MI, NI = P::NI;
+  // A tile of 256 rows with 128 or fewer in it takes half the products: the
+  // waves then share its columns alone, 128 x 64 each.  (For the weights'
+  // gradient, whose rows are many, it gained nothing.)
+  constexpr bool HALVES = BM == 256 && PASS != Pass::kWeight;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S * P::SLOT];
   __shared__ int prefix[PASS == Pass::kWeight ? 1 : kMaxRowMats];
   const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x >> 6));
@@ -215,12 +219,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   // (the caller has seen to it that the tiles stay below the limit: only
   // ranges that overlap, many times over, can have more)
   const int per_slice = min(mtiles, static_cast<int>(kMaxRowTiles / a.slices) / ntn) * ntn;
-  const int total = per_slice * a.slices;
+  const int tiles = per_slice * a.slices;
 
   // ---- which tiles are this workgroup's: runs of gridDim/8 consecutive
   // tiles go to one XCD (workgroups go to the XCDs round-robin), so that the
   // tiles that share rows or weights share an L2; few tiles are spread
   const int G = gridDim.x, b = blockIdx.x;
+  // If the last round of tiles would keep half of the workgroups busy at most,
+  // its tiles go to two workgroups each (8192 x 7168, sums of 4096, 3.5 rounds:
+  // 368 against 392 us)
+  const int rest = tiles % G;
+  const bool split = HALVES && 2 * rest <= G;
+  const int whole = split ? tiles - rest : tiles, total = split ? tiles + rest : tiles;
   const bool by_xcd = G % 8 == 0 && total > G;
   const int first = by_xcd ? (b & 7) * (G / 8) + (b >> 3) : b;
 
@@ -235,6 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   // row tiles, in a panel column block by column block
   auto tile_at = [&](int pos) -> TileAt {
     TileAt t;
+    int part = -1;  // of a tile that two workgroups share
+    if (pos >= whole) {
+      part = (pos - whole) & 1;
+      pos = whole + (pos - whole) / 2;
+    }
     t.slice = 0;
     if (a.slices > 1) {
       t.slice = uniform(static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(per_slice)));
@@ -273,6 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
       t.lo = 0;
       t.l = a.l;
     }
+    if (part >= 0) {
+      t.row0 += 128 * part;
+      t.rows = min(128, t.rows - 128 * part);  // (none left: nothing is stored)
+    }
     // (a tile without products has one step, of zeros)
     const int all = (t.l + 63) / 64, each = a.slices > 1 ? (all + a.slices - 1) / a.slices : all;
     t.step0 = t.slice * each;
@@ -282,22 +301,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
 
   // ---- issue side
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)lds));
-  int iss_pos = first, iss_left = 0, iss_rem = 0, iss_slot = 0;
+  int iss_pos = first, iss_tile = 0, iss_left = 0, iss_rem = 0, iss_slot = 0;
+  // What the other side will ask of a tile, the workgroup's n-th, in the lanes
+  // of one register: it is one or two tiles behind, and there are not enough
+  // scalar registers for so many tiles.
+  enum { kRow0, kRows, kCol0, kMat, kSlice, kSteps };
+  int tiles_at = 0;
+  auto get = [&](int n, int field) { return __builtin_amdgcn_readlane(tiles_at, (n & 3) * 8 + field); };
   uint64_t ia = 0, ib = 0;          // the step's first byte of each side
   v4i ra, rb;                       // and their buffers
   uint32_t oa[P::CA], ob[P::CB];
-  uint32_t out[2] = {0, 0};         // added to offsets past the end of L (plain sides)
+  uint32_t out[2] = {0, 0};         // set in offsets past the end of L (plain sides)
   const int ld2a = static_cast<int>(a.ld_a) * 2, ld2b = static_cast<int>(a.ld_b) * 2;
   const int64_t adv_a = TA ? int64_t(ld2a) * 64 : 128, adv_b = TB ? int64_t(ld2b) * 64 : 128;
   // (the copies of a wave begin at an even one, so a plain side's chunks alternate between two)
   static_assert(P::CA % 2 == 0 && P::CB % 2 == 0, "");
   const int chunk0 = (lane & 7) ^ ((lane >> 4) & 7);
   auto buffers = [&] {
-    ra = v4i{static_cast<int>(ia), static_cast<int>(ia >> 32), static_cast<int>(kNowhere), 0x00027000};
-    rb = v4i{static_cast<int>(ib), static_cast<int>(ib >> 32), static_cast<int>(kNowhere), 0x00027000};
     const int r = uniform(min(max(iss_rem, 0), 64));
-    if constexpr (TA) ra[2] = r * ld2a;
-    if constexpr (TB) rb[2] = r * ld2b;
+    ra = v4i{uniform(static_cast<int>(ia)), uniform(static_cast<int>(ia >> 32)), TA ? uniform(r * ld2a) : static_cast<int>(kNowhere), 0x00027000};
+    rb = v4i{uniform(static_cast<int>(ib)), uniform(static_cast<int>(ib >> 32)), TB ? uniform(r * ld2b) : static_cast<int>(kNowhere), 0x00027000};
     if constexpr (!TA || !TB) {
       out[0] = 8 * chunk0 >= iss_rem ? kNowhere : 0;
       out[1] = 8 * (chunk0 ^ 4) >= iss_rem ? kNowhere : 0;
@@ -315,21 +338,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
       ib = uniform(pb + t.e * a.mat_b + (PASS == Pass::kForward ? t.col0 * a.ld_b + l0 : l0 * a.ld_b + t.col0));
     }
     iss_left = t.steps;
+    const int n = iss_tile++;
+    auto put = [&](int field, int v) { tiles_at = lane == (n & 3) * 8 + field ? v : tiles_at; };
+    put(kRow0, t.row0);
+    put(kRows, t.rows);
+    put(kCol0, t.col0);
+    put(kMat, t.e);
+    put(kSlice, t.slice);
+    put(kSteps, t.steps);
     iss_rem = t.l - l0;
     const int cols = a.n - t.col0;
 #pragma unroll
     for (int q = 0; q < P::CA; ++q) {
       int row, chunk;
       SA::source(P::CA * wave + q, lane, row, chunk);
-      if constexpr (TA) oa[q] = 8 * chunk < t.rows ? row * ld2a + 16 * chunk : kNowhere;
-      else oa[q] = min(row, t.rows - 1) * ld2a + 16 * chunk;
+      // (rows that are not there come as zeros, which cost the matrix cores the least power)
+      oa[q] = (TA ? 8 * chunk : row) < t.rows ? row * ld2a + 16 * chunk : kNowhere;
     }
 #pragma unroll
     for (int q = 0; q < P::CB; ++q) {
       int row, chunk;
       SB::source(P::CB * wave + q, lane, row, chunk);
-      if constexpr (TB) ob[q] = 8 * chunk < cols ? row * ld2b + 16 * chunk : kNowhere;
-      else ob[q] = min(row, cols - 1) * ld2b + 16 * chunk;
+      ob[q] = (TB ? 8 * chunk : row) < cols ? row * ld2b + 16 * chunk : kNowhere;
     }
     buffers();
   };
@@ -339,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   auto issue = [&](auto mc) {
     constexpr int m = decltype(mc)::value;
     const uint32_t slot = lds0 + iss_slot * P::SLOT;
-    if constexpr (m < P::CA) copy16(TA ? oa[m] : oa[m] + out[m % 2], ra, slot + P::A + (P::CA * wave + m) * 1024);
-    else copy16(TB ? ob[m - P::CA] : ob[m - P::CA] + out[m % 2], rb, slot + P::B + (P::CB * wave + m - P::CA) * 1024);
+    if constexpr (m < P::CA) copy16(TA ? oa[m] : oa[m] | out[m % 2], ra, slot + P::A + (P::CA * wave + m) * 1024);
+    else copy16(TB ? ob[m - P::CA] : ob[m - P::CA] | out[m % 2], rb, slot + P::B + (P::CB * wave + m - P::CA) * 1024);
   };
   // to the next step; behind the last tile the last one is copied again, into
   // slots that are not read
@@ -359,10 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
 
   // ---- read side: byte offsets in a slot of this lane's fragments
   int fa[TA ? MI : 1], fb[TB ? NI : 1];
+  auto set_frags = [&](bool half) {
+    const int a0 = half ? 0 : wm * MI, b0 = half ? wave * (NI / 2) : wn * NI;
 #pragma unroll
-  for (int i = 0; i < (TA ? MI : 1); ++i) fa[i] = P::A + SA::frag(wm * MI + i, lane);
+    for (int i = 0; i < (TA ? MI : 1); ++i) fa[i] = P::A + SA::frag(a0 + i, lane);
+    // (of half a tile only the first NI/2 are there; the others' reads stay in the slot)
 #pragma unroll
-  for (int j = 0; j < (TB ? NI : 1); ++j) fb[j] = P::B + SB::frag(wn * NI + j, lane);
+    for (int j = 0; j < (TB ? NI : 1); ++j) fb[j] = P::B + SB::frag((b0 + j) % (kRowsTileN / 32), lane);
+  };
   // plain: quarter h of a step is chunks 2h and 2h + 1
   const int sw = (l32 >> 1) & 7;
   const int ch[4] = {16 * (g32 ^ sw), 16 * ((2 + g32) ^ sw), 16 * ((4 + g32) ^ sw), 16 * ((6 + g32) ^ sw)};
@@ -386,21 +420,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
     }
   };
 
-  v16f acc[MI][NI];
-  // The products so far stay before this point (without it the compiler moves
-  // them past the branches below, to where the sums are next used).
-  auto settle = [&] {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j) asm volatile("" : "+a"(acc[i][j]));
-  };
   int slot = 0;
   // One step of four quarters.  FIRST: the tile's first, its products start
   // from zero.  after_stores: the last tile's stores may still be on their way
   // (operations finish in the order in which they were issued).
-  auto step = [&](auto first_c, bool after_stores) {
+  // acc: the sums, MI x NI blocks or half as many.  last: the last of tile n.
+  auto step = [&](auto first_c, auto& acc, bool after_stores, bool last, int n) {
     constexpr bool FIRST = decltype(first_c)::value != 0;
+    constexpr int NE = sizeof(acc[0]) / sizeof(v16f), NM = MI * NE;
+    // The products so far stay before this point (without it the compiler moves
+    // them past the branches below, to where the sums are next used).
+    auto settle = [&] {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NE; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
     const int nslot = slot + 1 == S ? 0 : slot + 1;
     // the copies of step s + S - 1, begun in the last quarter of step s - 1,
     // go on over the quarters before the barrier (with two slots: the first)
@@ -422,9 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
         if (S > 2 && after_stores) wait_vm<(left + P::STORES < 63 ? left + P::STORES : 63)>();
         else wait_vm<left>();
         tile_barrier();
+        if constexpr (HALVES)
+          if (last) set_frags(get(n + 1, kRows) <= 128);
       }
       unrolled<0, NM>([&](auto kc) {
-        constexpr int k = decltype(kc)::value, i = k / NI, j = k % NI;
+        constexpr int k = decltype(kc)::value, i = k / NE, j = k % NE;
         acc[i][j] = mfma32<T>(bv[q % 2][j], av[q % 2][i], FIRST && q == 0 ? v16f{} : acc[i][j]);
         // the next quarter's reads, in the first three quarters of this one
         constexpr int R = MI + NI, lo = k * R / (NM * 3 / 4), hi = (k + 1) * R / (NM * 3 / 4);
@@ -448,30 +485,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   // takes an offset past the buffer's end and stores nothing, so there are no
   // branches (which would cost copies of the accumulators).  Otherwise the
   // same 16-byte pieces at any address, and only a row's last one by elements.
-  auto store_tile = [&](const TileAt& t) {
+  auto store_tile = [&](int n, auto& acc) {
+    constexpr int NE = sizeof(acc[0]) / sizeof(v16f);
+    constexpr bool HALF = NE < NI;
     constexpr int SZ = sizeof(TO), PER = 16 / SZ;
-    const uint64_t base = uniform(static_cast<TO*>(a.c) + t.slice * a.slice_c +
-                                  (PASS == Pass::kWeight ? t.e * a.mat_c : 0) + int64_t(t.row0) * a.ld_c + t.col0);
+    const int rows = get(n, kRows), col0 = get(n, kCol0), cols = a.n - col0;
+    const uint64_t base = uniform(static_cast<TO*>(a.c) + get(n, kSlice) * a.slice_c +
+                                  (PASS == Pass::kWeight ? get(n, kMat) * a.mat_c : 0) + get(n, kRow0) * a.ld_c + col0);
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, kNowhere, 0x00027000);
-    const int cols = a.n - t.col0;
     const uint32_t ld = static_cast<uint32_t>(a.ld_c) * SZ;
     // the last MFMA's results take 16 passes (18 wait states); the compiler
     // counts them for its own reads, not for the assembly's below
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     // this lane's rows: with 16-bit results lane l stores rows l%16 and
     // 16 + l%16 of each block of 32, otherwise row l%32
-    constexpr bool HALVES = SZ == 2;
-    constexpr int NR = HALVES ? 2 : 1;
+    constexpr bool ROWS16 = SZ == 2;
+    constexpr int NR = ROWS16 ? 2 : 1;
     uint32_t at[MI][NR];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int h = 0; h < NR; ++h) {
-        const int row = (wm * MI + i) * 32 + (HALVES ? 16 * h + (lane & 15) : l32);
-        at[i][h] = row < t.rows ? row * ld : kNowhere;
+        const int row = ((HALF ? 0 : wm * MI) + i) * 32 + (ROWS16 ? 16 * h + (lane & 15) : l32);
+        at[i][h] = row < rows ? row * ld : kNowhere;
       }
-    unrolled<0, NM>([&](auto bc) {
-      constexpr int i = decltype(bc)::value / NI, j = decltype(bc)::value % NI;
+    unrolled<0, MI * NE>([&](auto bc) {
+      constexpr int i = decltype(bc)::value / NE, j = decltype(bc)::value % NE;
       typedef uint32_t v4u __attribute__((ext_vector_type(4)));
       const v16f& r = acc[i][j];
       // result x of the block out of its accumulator register, here and not
@@ -501,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
           }
         }
       };
-      const int col = (wn * NI + j) * 32;
-      if constexpr (HALVES) {
+      const int col = (HALF ? wave * NE + j : wn * NI + j) * 32;
+      if constexpr (ROWS16) {
         // lane (l32, g32) has columns 8q + 4 g32 .. + 3 of row l32, q = 0..3.
         // Lanes l and l + 32 exchange halves, and it has 8 columns (16 bytes),
         // 16p + 8 g32 .., p = 0, 1; then the 16-lane rows of the wave do, and
@@ -541,25 +580,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   if (first < total) {
     // ---- the stream of steps: the first S - 1 and the first part of the next
     // are on their way before the first product
-    iss_setup(tile_at(iss_pos));
+    iss_setup(tile_at(first));
     unrolled<0, S - 1>([&](auto) {
       unrolled<0, P::C>([&](auto mc) { issue(mc); });
       advance();
     });
     unrolled<0, P::C0>([&](auto mc) { issue(mc); });
+    set_frags(HALVES && get(0, kRows) <= 128);
     wait_vm<P::C*(S - 2) + P::C0>();
     tile_barrier();
     unrolled<0, MI + NI>([&](auto jc) { read_frag(0, Int<0>{}, jc); });
 
     bool stored = false;
-    for (int pos = first; pos < total; pos = next_pos(pos)) {
-      const TileAt t = tile_at(pos);
+    int n = 0;
+    for (int pos = first; pos < total; pos = next_pos(pos), ++n) {
       // without WIDE the number of stores is not known here: wait for all
       if (!WIDE && stored) wait_vm<0>();
       stored &= WIDE;
-      step(Int<1>{}, stored);
-      for (int s = 1; s < t.steps; ++s) step(Int<0>{}, false);
-      store_tile(t);
+      auto run = [&](auto ne) {
+        v16f acc[MI][decltype(ne)::value];
+        int left = get(n, kSteps) - 1;
+        step(Int<1>{}, acc, stored, left == 0, n);
+        while (left > 0) step(Int<0>{}, acc, false, --left == 0, n);
+        store_tile(n, acc);
+      };
+      if (HALVES && get(n, kRows) <= 128) run(Int<HALVES ? NI / 2 : NI>{});
+      else run(Int<NI>{});
       stored = true;
     }
     // the copies still on their way land in this workgroup's LDS
