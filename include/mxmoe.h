@@ -391,53 +391,52 @@ moe_status moe_combine_rows_backward(const void *dy, const void *rows, moe_src_d
  * For training, or for weights that are not quantised: rows sorted by expert
  * times bf16 or fp16 matrices, forwards and backwards.  Errors and streams as
  * for the pieces above. */
-typedef enum { MOE_ROWS_FORWARD = 0, MOE_ROWS_INPUT = 1, MOE_ROWS_WEIGHT = 2 } moe_rows_pass;
 
 /* With W_e the matrix of the rows offsets[e] <= r < offsets[e+1] (w [mats][n][k]):
- *   moe_linear_rows     y[r][j]    = sum over i of x[r][i] W_e[j][i]
- *   moe_linear_rows_dx  dx[r][i]   = sum over j of dy[r][j] W_e[j][i]
- *   moe_linear_rows_dw  dW_e[j][i] = sum over e's rows r of dy[r][j] x[r][i]
+ *   moe_linear_rows           y[r][j]    = sum over i of x[r][i] W_e[j][i]
+ *   moe_linear_rows_backward  dx[r][i]   = sum over j of dy[r][j] W_e[j][i]
+ *                             dW_e[j][i] = sum over e's rows r of dy[r][j] x[r][i]
  * Sums in fp32 in a fixed order, rounded once to the result's type: dt, and
  * for dw dt or fp32.  dt: bf16 or fp16 (fp32: MOE_ERR_UNSUPPORTED).
  * x [rows][ld_x], dy [rows][ld_dy], y [rows][ld_y], dx [rows][ld_dx], strides
  * in elements; w and dw dense.  offsets as in moe_linear_mx4 (NULL: mats must
- * be 1, and all rows take it).  Rows of no matrix are zero in y and dx and are
- * not read for dw; a matrix without rows has a zero gradient.  An empty sum
- * (k, n or rows 0) is zero.
+ * be 1, and all rows take it).  Rows before the first that a matrix has and
+ * behind the last are zero in y and dx and are not read for dw (offsets that
+ * decrease can leave out others, which are then undefined); a matrix without
+ * rows has a zero gradient.  An empty sum (k, n or rows 0) is zero.
+ * backward: dx or dw NULL: that gradient is left out; w is read for dx only,
+ * x for dw only.  x may come in 8 bits instead (x NULL, ld_x 0): x_codes
+ * [rows][k] and x_scales [rows][ceil(k/32)] as moe_quantize_mx8 makes them,
+ * taken by their values in dt; the workspace then holds those.
  * 0 <= rows <= 2^25; 0 <= n, k <= 2^20; 1 <= mats <= 1024; strides at most
  * 2^21; at most 2^30 tiles of 64 rows (dw: 128 of n) x 256 columns, counted
  * for each matrix.
  * x, dy and w 16-byte aligned, offsets 4-byte, results aligned to their
  * element (an fp32 dw to 16 bytes).
- * workspace: moe_linear_rows_workspace_bytes bytes (0: it may be NULL),
- * 256-byte aligned, contents on entry irrelevant; concurrent calls need
- * distinct workspaces.  It holds fp32 sums of parts where few results have
- * long sums, and copies of operands whose rows are not whole numbers of 16
- * bytes: widths and strides that are multiples of 8 are the fast case.  Its
- * arguments are the call's own: ld_a the stride of x (forward) or dy, ld_x
- * that of x for dw (else 0), grouped whether offsets are given, out_dt the
- * result's type, ld_out its stride (dw: k).
- * x of dw may come in 8 bits instead (x NULL, ld_x 0): x_codes [rows][k] and
- * x_scales [rows][ceil(k/32)] as moe_quantize_mx8 makes them, taken by their
- * values in dt; the workspace then holds those. */
-moe_status moe_linear_rows_workspace_bytes(moe_rows_pass pass, moe_src_dtype dt, int64_t rows,
-                                           int64_t ld_a, int64_t ld_x, int32_t mats,
-                                           int32_t grouped, int64_t n, int64_t k,
-                                           moe_src_dtype out_dt, int64_t ld_out,
-                                           size_t *out_bytes);
+ * workspace: as many bytes as the call's query says for the same arguments
+ * (0: it may be NULL; grouped: whether offsets are given), 256-byte aligned,
+ * contents on entry irrelevant; concurrent calls need distinct workspaces.  It
+ * holds fp32 sums of parts where few results have long sums, and copies of
+ * operands whose rows are not whole numbers of 16 bytes: widths and strides
+ * that are multiples of 8 are the fast case. */
+moe_status moe_linear_rows_workspace_bytes(moe_src_dtype dt, int64_t rows, int64_t ld_x,
+                                           int32_t mats, int32_t grouped, int64_t n, int64_t k,
+                                           int64_t ld_y, size_t *out_bytes);
 moe_status moe_linear_rows(const void *x, moe_src_dtype dt, int64_t rows, int64_t ld_x,
                            const void *w, int32_t mats, const int32_t *offsets, int64_t n,
                            int64_t k, void *y, int64_t ld_y, void *workspace,
                            size_t workspace_bytes, void *stream);
-moe_status moe_linear_rows_dx(const void *dy, moe_src_dtype dt, int64_t rows, int64_t ld_dy,
-                              const void *w, int32_t mats, const int32_t *offsets, int64_t n,
-                              int64_t k, void *dx, int64_t ld_dx, void *workspace,
-                              size_t workspace_bytes, void *stream);
-moe_status moe_linear_rows_dw(const void *dy, moe_src_dtype dt, int64_t rows, int64_t ld_dy,
-                              const void *x, int64_t ld_x, const uint8_t *x_codes,
-                              const uint8_t *x_scales, int32_t mats, const int32_t *offsets,
-                              int64_t n, int64_t k, void *dw, moe_src_dtype dw_dt,
-                              void *workspace, size_t workspace_bytes, void *stream);
+moe_status moe_linear_rows_backward_workspace_bytes(moe_src_dtype dt, int64_t rows, int64_t ld_dy,
+                                                    int64_t ld_x, int32_t mats, int32_t grouped,
+                                                    int64_t n, int64_t k, int32_t want_dx,
+                                                    int64_t ld_dx, int32_t want_dw,
+                                                    moe_src_dtype dw_dt, size_t *out_bytes);
+moe_status moe_linear_rows_backward(const void *dy, moe_src_dtype dt, int64_t rows, int64_t ld_dy,
+                                    const void *x, int64_t ld_x, const uint8_t *x_codes,
+                                    const uint8_t *x_scales, const void *w, int32_t mats,
+                                    const int32_t *offsets, int64_t n, int64_t k, void *dx,
+                                    int64_t ld_dx, void *dw, moe_src_dtype dw_dt, void *workspace,
+                                    size_t workspace_bytes, void *stream);
 
 /* Activations kept in 8 bits until the backward pass.  MXFP8 of the rows of a
  * bf16, fp16 or fp32 matrix of any width: per row and per 32 consecutive

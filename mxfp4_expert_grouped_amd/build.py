@@ -32,7 +32,7 @@ LIBS = {
     "libmxmoe.so": ["api.cpp", "kernels_route.hip", "kernels_gemm.hip", "kernels_pack.hip",
                     "kernels_tail.hip", "kernels_mx4.hip", "kernels_linear.hip", "kernels_tokens.hip",
                     "kernels_rows_forward.hip", "kernels_rows_input.hip", "kernels_rows_weight.hip",
-                    "kernels_rows_aux.hip", "kernels_glu.hip"],
+                    "kernels_rows_stream.hip", "kernels_rows_aux.hip", "kernels_glu.hip"],
     "libmxmoe_inputs.so": ["gen_inputs.hip"],
 }
 

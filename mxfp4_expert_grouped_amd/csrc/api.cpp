@@ -854,170 +854,250 @@ namespace {
 
 using rows::Pass;
 
-// One product as its entry point was called: sizes, row strides (elements)
-// and the pieces of its workspace.
+// A call of the products, forwards or backwards: its checked sizes, the kernels
+// that its passes take and the pieces of its workspace.
 struct RowsCall {
-  rows::RowsShape s;
-  rows::RowsChoice c;
-  // operands that are laid out in the workspace first, rows on 16 bytes
-  bool pad_a, pad_b;
-  bool codes;                        // x of the weights' gradient comes in 8 bits (and is laid out so)
-  int64_t ld_a, ld_b;                // row strides of the operands as the kernels read them
-  size_t off_a, off_b, off_part, total;
+  RowType t;
+  int mats;
+  bool grouped;
+  int64_t rows, n, k;
+  bool codes;                          // x of the weights' gradient comes in 8 bits
+  // operands that are laid out in the workspace first, rows on 16 bytes, and
+  // the row strides that the kernels then see
+  bool pad_x, pad_w, pad_dy;
+  int64_t ld_x, ld_w, ld_dy;
+  size_t off_x, off_w, off_dy, off_part, total;
+  rows::RowsShape shape[3];            // by pass
+  rows::RowsChoice choice[3];
 };
 
-// Checks of what does not depend on pointers; -> the call's layout.  a: x or
-// dy, ld_a apart; for the weights' gradient ld_x is the stride of x, 0 where
-// it comes in 8 bits.
-moe_status plan_rows(moe_rows_pass pass, moe_src_dtype dt, int64_t nrows, int64_t ld_a, int64_t ld_x, int32_t mats, bool grouped,
-                     int64_t n, int64_t k, moe_src_dtype out_dt, int64_t ld_out, RowsCall& p) {
-  if (pass != MOE_ROWS_FORWARD && pass != MOE_ROWS_INPUT && pass != MOE_ROWS_WEIGHT) return fail(MOE_ERR_INVALID_ARG, "bad pass");
-  if (dt != MOE_SRC_BF16 && dt != MOE_SRC_FP16)
-    return fail(dt == MOE_SRC_FP32 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG, "the products take bf16 and fp16");
-  if (out_dt != dt && !(pass == MOE_ROWS_WEIGHT && out_dt == MOE_SRC_FP32)) return fail(MOE_ERR_INVALID_ARG, "bad type of the result");
+moe_status check_rows(moe_src_dtype dt, int64_t nrows, int32_t mats, bool grouped, int64_t n, int64_t k, RowsCall& p) {
+  int64_t sz;
+  if (!row_type(dt, p.t, sz)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
+  if (dt == MOE_SRC_FP32) return fail(MOE_ERR_UNSUPPORTED, "the products take bf16 and fp16");
   if (nrows < 0 || n < 0 || k < 0 || mats <= 0) return fail(MOE_ERR_INVALID_ARG, "negative size, or mats not positive");
   if (!grouped && mats != 1) return fail(MOE_ERR_INVALID_ARG, "%d matrices need offsets", mats);
   if (mats > rows::kMaxRowMats || n > (1 << 20) || k > (1 << 20) || nrows > (1 << 25))
     return fail(MOE_ERR_UNSUPPORTED, "more than 1024 matrices, 2^20 columns or 2^25 rows");
-  const int64_t wa = pass == MOE_ROWS_FORWARD ? k : n, wo = pass == MOE_ROWS_FORWARD ? n : k;
-  p.codes = pass == MOE_ROWS_WEIGHT && ld_x == 0;
-  if (ld_a < wa || (pass == MOE_ROWS_WEIGHT && !p.codes && ld_x < k) || (pass != MOE_ROWS_WEIGHT && ld_out < wo))
-    return fail(MOE_ERR_INVALID_ARG, "row stride below the row's width");
-  if (ld_a > (1 << 21) || ld_x > (1 << 21) || ld_out > (1 << 21)) return fail(MOE_ERR_UNSUPPORTED, "row stride above 2^21");
-  const int64_t tn = rows::ceil_div(wo, rows::kRowsTileN);
-  const int64_t tiles = pass == MOE_ROWS_WEIGHT ? mats * rows::ceil_div(n, 128) * tn : (rows::ceil_div(nrows, 64) + mats) * tn;
-  if (tiles > rows::kMaxRowTiles) return fail(MOE_ERR_UNSUPPORTED, "more than 2^30 tiles");
-  const int osz = out_dt == MOE_SRC_FP32 ? 4 : 2;
-  p.s = {pass == MOE_ROWS_FORWARD ? Pass::kForward : pass == MOE_ROWS_INPUT ? Pass::kInput : Pass::kWeight,
-         nrows, n, k, mats, grouped, osz, wo % (16 / osz) == 0 && ld_out % (16 / osz) == 0};
-  p.c = rows::choose_rows(p.s);
-  // rows of whole pieces of 16 bytes are read where they are
-  p.pad_a = wa % 8 || ld_a % 8;
-  p.pad_b = p.codes || (pass == MOE_ROWS_WEIGHT ? (k % 8 || ld_x % 8) : k % 8 != 0);
-  p.ld_a = p.pad_a ? rows::round8(wa) : ld_a;
-  p.ld_b = p.pad_b ? rows::round8(k) : pass == MOE_ROWS_WEIGHT ? ld_x : k;
+  p.mats = mats;
+  p.grouped = grouped;
+  p.rows = nrows;
+  p.n = n;
+  p.k = k;
+  return MOE_OK;
+}
+
+moe_status check_stride(int64_t ld, int64_t width) {
+  if (ld < width) return fail(MOE_ERR_INVALID_ARG, "row stride below the row's width");
+  if (ld > (1 << 21)) return fail(MOE_ERR_UNSUPPORTED, "row stride above 2^21");
+  return MOE_OK;
+}
+
+// The kernel of one pass, whose result has elements of out_size bytes in rows ld_out apart.
+moe_status choose_pass(RowsCall& p, Pass pass, int out_size, int64_t ld_out) {
+  rows::RowsShape& s = p.shape[static_cast<int>(pass)];
+  s.pass = pass;
+  s.rows = p.rows;
+  s.n = p.n;
+  s.k = p.k;
+  s.mats = p.mats;
+  s.grouped = p.grouped;
+  s.out_size = out_size;
+  s.laid_out = pass == Pass::kForward ? (p.pad_x ? p.rows * p.k : 0) + (p.pad_w ? p.mats * p.n * p.k : 0) : 0;
+  s.pieces = s.cols() % (16 / out_size) == 0 && ld_out % (16 / out_size) == 0;
+  if (rows::least_tiles(s) > rows::kMaxRowTiles) return fail(MOE_ERR_UNSUPPORTED, "more than 2^30 tiles");
+  p.choice[static_cast<int>(pass)] = rows::choose_rows(s);
+  return MOE_OK;
+}
+
+// The workspace: operands that are laid out, and the sums of one pass at a time.
+void lay_out(RowsCall& p, bool forward, bool input, bool weight) {
   size_t at = 0;
   auto take = [&](bool used, int64_t bytes) {
     const size_t o = at;
     if (used) at += (size_t(bytes) + 255) & ~size_t(255);
     return o;
   };
-  p.off_a = take(p.pad_a, nrows * p.ld_a * 2);
-  p.off_b = take(p.pad_b, (pass == MOE_ROWS_WEIGHT ? nrows : mats * n) * p.ld_b * 2);
-  p.off_part = take(p.c.join, rows::join_rows(p.s) * rows::join_ld(p.s) * p.c.slices * 4);
+  p.off_x = take(p.pad_x, p.rows * p.ld_x * 2);
+  p.off_w = take(p.pad_w, p.mats * p.n * p.ld_w * 2);
+  p.off_dy = take(p.pad_dy, p.rows * p.ld_dy * 2);
+  const bool used[3] = {forward, input, weight};
+  int64_t part = 0;
+  for (int i = 0; i < 3; ++i)
+    if (used[i] && p.choice[i].join)
+      part = std::max(part, rows::join_rows(p.shape[i]) * rows::join_ld(p.shape[i]) * p.choice[i].slices * 4);
+  p.off_part = take(part > 0, part);
   p.total = at;
+}
+
+moe_status plan_forward(moe_src_dtype dt, int64_t nrows, int64_t ld_x, int32_t mats, bool grouped, int64_t n, int64_t k, int64_t ld_y,
+                        RowsCall& p) {
+  p = RowsCall{};
+  moe_status s = check_rows(dt, nrows, mats, grouped, n, k, p);
+  if (s == MOE_OK) s = check_stride(ld_x, k);
+  if (s == MOE_OK) s = check_stride(ld_y, n);
+  if (s != MOE_OK) return s;
+  p.pad_x = k % 8 || ld_x % 8;
+  p.pad_w = k % 8;
+  s = choose_pass(p, Pass::kForward, 2, ld_y);
+  if (s != MOE_OK) return s;
+  if (p.choice[0].stream) p.pad_x = p.pad_w = false;
+  p.ld_x = p.pad_x ? rows::round8(k) : ld_x;
+  p.ld_w = p.pad_w ? rows::round8(k) : k;
+  lay_out(p, true, false, false);
   return MOE_OK;
 }
 
-// Runs the product: a as above, b is w or x (its codes, with x_scales).
-moe_status run_rows(RowsCall& p, moe_src_dtype dt, const void* a, int64_t ld_a, const void* b, int64_t ld_b, const uint8_t* x_scales,
-                    const int32_t* offsets, void* out, moe_src_dtype out_dt, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
-  const rows::RowsShape& s = p.s;
-  const bool weight = s.pass == Pass::kWeight;
-  if (!aligned(a, 16) || (!p.codes && !aligned(b, 16)) || !aligned(out, s.out_size) || !aligned(offsets, 4))
-    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer (operands: 16 bytes; offsets: 4; the result: its element, 16 bytes as fp32)");
-  if (s.out_size == 4 && !aligned(out, 16)) return fail(MOE_ERR_INVALID_ARG, "an fp32 result needs 16-byte alignment");
-  if (p.total && (!workspace || workspace_bytes < p.total))
-    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s", p.total, workspace_bytes, workspace ? "" : " (NULL)");
+// ld_x 0: x comes in 8 bits
+moe_status plan_backward(moe_src_dtype dt, int64_t nrows, int64_t ld_dy, int64_t ld_x, int32_t mats, bool grouped, int64_t n, int64_t k,
+                         bool input, int64_t ld_dx, bool weight, moe_src_dtype dw_dt, RowsCall& p) {
+  p = RowsCall{};
+  moe_status s = check_rows(dt, nrows, mats, grouped, n, k, p);
+  if (s == MOE_OK) s = check_stride(ld_dy, n);
+  p.codes = weight && ld_x == 0;
+  if (s == MOE_OK && weight && !p.codes) s = check_stride(ld_x, k);
+  if (s == MOE_OK && input) s = check_stride(ld_dx, k);
+  if (s != MOE_OK) return s;
+  if (weight && dw_dt != dt && dw_dt != MOE_SRC_FP32) return fail(MOE_ERR_INVALID_ARG, "dw is of dy's type or fp32");
+  p.pad_dy = n % 8 || ld_dy % 8;
+  p.pad_w = input && k % 8;
+  p.pad_x = weight && (p.codes || k % 8 || ld_x % 8);
+  p.ld_dy = p.pad_dy ? rows::round8(n) : ld_dy;
+  p.ld_w = p.pad_w ? rows::round8(k) : k;
+  p.ld_x = p.pad_x ? rows::round8(k) : ld_x;
+  if (input) s = choose_pass(p, Pass::kInput, 2, ld_dx);
+  if (s == MOE_OK && weight) s = choose_pass(p, Pass::kWeight, dw_dt == MOE_SRC_FP32 ? 4 : 2, k);
+  if (s != MOE_OK) return s;
+  lay_out(p, false, input, weight);
+  return MOE_OK;
+}
+
+moe_status check_workspace(const RowsCall& p, const void* workspace, size_t bytes) {
+  if (p.total && (!workspace || bytes < p.total))
+    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s", p.total, bytes, workspace ? "" : " (NULL)");
   if (p.total && !aligned(workspace, 256)) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  int num_cus = 0;
-  moe_status st = check_device(&num_cus);
-  if (st != MOE_OK) return st;
-  if (!p.c.join && s.pieces && !aligned(out, 16)) p.c.wide = false;
-  RowType t, ot;
-  int64_t sz;
-  row_type(dt, t, sz);
-  row_type(out_dt, ot, sz);
-  const hipStream_t hs = static_cast<hipStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
-  hipError_t e = hipSuccess;
-  if (p.pad_a) {
-    e = rows::launch_pad_rows(a, s.rows, s.pass == Pass::kForward ? s.k : s.n, ld_a, ws + p.off_a, p.ld_a, hs);
-    a = ws + p.off_a;
-  }
-  if (p.pad_b && e == hipSuccess) {
-    e = p.codes ? launch_dequantize_mx8(static_cast<const uint8_t*>(b), x_scales, s.rows, s.k, ws + p.off_b, t, p.ld_b, p.ld_b, hs)
-                : rows::launch_pad_rows(b, weight ? s.rows : s.mats * s.n, s.k, ld_b, ws + p.off_b, p.ld_b, hs);
-    b = ws + p.off_b;
-  }
-  if (e != hipSuccess) return launched(e);
-  const int64_t cols = s.cols();
+  return MOE_OK;
+}
+
+// One pass on operands as they lie now.
+hipError_t run_pass(const RowsCall& p, Pass pass, const void* a, int64_t ld_a, const void* b, int64_t ld_b, const int32_t* offsets,
+                    void* out, RowType out_t, int64_t ld_out, char* ws, int num_cus, hipStream_t st) {
+  const rows::RowsShape& s = p.shape[static_cast<int>(pass)];
+  rows::RowsChoice c = p.choice[static_cast<int>(pass)];
+  if (!c.join && c.wide && !aligned(out, 16)) c.wide = false;
+  const bool weight = pass == Pass::kWeight;
   rows::RowsArgs r{};
-  r.a = a; r.ld_a = p.ld_a;
-  r.b = b; r.ld_b = p.ld_b; r.mat_b = s.n * p.ld_b;
-  r.offsets = offsets; r.rows = s.rows; r.mats = s.mats;
-  r.m = static_cast<int>(s.n);
-  r.n = static_cast<int>(cols);
-  r.l = static_cast<int>(s.pass == Pass::kForward ? s.k : s.n);
-  r.slices = p.c.slices;
+  r.a = a; r.ld_a = ld_a;
+  r.b = b; r.ld_b = ld_b; r.mat_b = p.n * ld_b;
+  r.offsets = offsets; r.rows = p.rows; r.mats = p.mats;
+  r.m = static_cast<int>(p.n);
+  r.n = static_cast<int>(s.cols());
+  r.l = static_cast<int>(pass == Pass::kForward ? p.k : p.n);
+  r.slices = c.slices;
   r.num_cus = num_cus > 0 ? num_cus : 256;
-  if (p.c.join) {
-    r.c = ws + p.off_part;
-    r.ld_c = rows::join_ld(s);
-    r.slice_c = rows::join_rows(s) * r.ld_c;
-  } else {
-    r.c = out;
-    r.ld_c = ld_out;
-  }
-  r.mat_c = s.n * r.ld_c;
-  const RowType ct = p.c.join ? RowType::kFp32 : ot;
-  switch (s.pass) {
-    case Pass::kForward: e = rows::launch_forward(r, p.c, t, ct, hs); break;
-    case Pass::kInput: e = rows::launch_input(r, p.c, t, ct, hs); break;
-    default: e = rows::launch_weight(r, p.c, t, ct, hs);
-  }
-  if (e == hipSuccess && p.c.join)
-    e = rows::launch_join(static_cast<const float*>(r.c), p.c.slices, rows::join_rows(s), cols, r.ld_c, weight ? nullptr : offsets,
-                          s.mats, out, ot, ld_out, hs);
-  return launched(e);
+  r.c = c.join ? ws + p.off_part : out;
+  r.ld_c = c.join ? rows::join_ld(s) : ld_out;
+  r.mat_c = p.n * r.ld_c;
+  r.slice_c = c.join ? rows::join_rows(s) * r.ld_c : 0;
+  const RowType ct = c.join ? RowType::kFp32 : out_t;
+  const hipError_t e = c.stream                    ? rows::launch_stream(r, c, p.t, st)
+                       : pass == Pass::kForward ? rows::launch_forward(r, c, p.t, ct, st)
+                       : pass == Pass::kInput   ? rows::launch_input(r, c, p.t, ct, st)
+                                                : rows::launch_weight(r, c, p.t, ct, st);
+  if (e != hipSuccess || !c.join) return e;
+  return rows::launch_join(static_cast<const float*>(r.c), c.slices, rows::join_rows(s), s.cols(), r.ld_c,
+                           weight ? nullptr : offsets, p.mats, out, out_t, ld_out, st);
 }
 
 }  // namespace
 
 extern "C" {
 
-moe_status moe_linear_rows_workspace_bytes(moe_rows_pass pass, moe_src_dtype dt, int64_t num_rows, int64_t ld_a, int64_t ld_x,
-                                           int32_t mats, int32_t grouped, int64_t n, int64_t k, moe_src_dtype out_dt, int64_t ld_out,
-                                           size_t* out_bytes) {
+moe_status moe_linear_rows_workspace_bytes(moe_src_dtype dt, int64_t num_rows, int64_t ld_x, int32_t mats, int32_t grouped, int64_t n,
+                                           int64_t k, int64_t ld_y, size_t* out_bytes) {
   if (!out_bytes) return fail(MOE_ERR_INVALID_ARG, "out_bytes is NULL");
   RowsCall p;
-  moe_status s = plan_rows(pass, dt, num_rows, ld_a, ld_x, mats, grouped != 0, n, k, out_dt, ld_out, p);
-  if (s != MOE_OK) return s;
-  *out_bytes = p.total;
-  return MOE_OK;
+  const moe_status s = plan_forward(dt, num_rows, ld_x, mats, grouped != 0, n, k, ld_y, p);
+  if (s == MOE_OK) *out_bytes = p.total;
+  return s;
 }
 
 moe_status moe_linear_rows(const void* x, moe_src_dtype dt, int64_t num_rows, int64_t ld_x, const void* w, int32_t mats,
                            const int32_t* offsets, int64_t n, int64_t k, void* y, int64_t ld_y, void* workspace,
                            size_t workspace_bytes, void* stream) {
   RowsCall p;
-  moe_status s = plan_rows(MOE_ROWS_FORWARD, dt, num_rows, ld_x, 0, mats, offsets != nullptr, n, k, dt, ld_y, p);
+  moe_status s = plan_forward(dt, num_rows, ld_x, mats, offsets != nullptr, n, k, ld_y, p);
   if (s != MOE_OK || num_rows == 0 || n == 0) return s;
   if (!y || (k > 0 && (!x || !w))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
-  return run_rows(p, dt, x, ld_x, w, k, nullptr, offsets, y, dt, ld_y, workspace, workspace_bytes, stream);
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2) || !aligned(offsets, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer (x and w: 16 bytes; offsets: 4; y: its element)");
+  s = check_workspace(p, workspace, workspace_bytes);
+  int num_cus = 0;
+  if (s == MOE_OK) s = check_device(&num_cus);
+  if (s != MOE_OK) return s;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  rows::PadMatrix pads[rows::kMaxPads];
+  int count = 0;
+  if (p.pad_x) pads[count++] = {x, num_rows, k, ld_x, ws + p.off_x, p.ld_x};
+  if (p.pad_w) pads[count++] = {w, mats * n, k, k, ws + p.off_w, p.ld_w};
+  if (count) {
+    const hipError_t e = rows::launch_pad_rows(pads, count, st);
+    if (e != hipSuccess) return launched(e);
+  }
+  return launched(run_pass(p, Pass::kForward, p.pad_x ? ws + p.off_x : x, p.ld_x, p.pad_w ? ws + p.off_w : w, p.ld_w, offsets, y, p.t,
+                           ld_y, ws, num_cus, st));
 }
 
-moe_status moe_linear_rows_dx(const void* dy, moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, const void* w, int32_t mats,
-                              const int32_t* offsets, int64_t n, int64_t k, void* dx, int64_t ld_dx, void* workspace,
-                              size_t workspace_bytes, void* stream) {
+moe_status moe_linear_rows_backward_workspace_bytes(moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, int64_t ld_x, int32_t mats,
+                                                    int32_t grouped, int64_t n, int64_t k, int32_t want_dx, int64_t ld_dx,
+                                                    int32_t want_dw, moe_src_dtype dw_dt, size_t* out_bytes) {
+  if (!out_bytes) return fail(MOE_ERR_INVALID_ARG, "out_bytes is NULL");
   RowsCall p;
-  moe_status s = plan_rows(MOE_ROWS_INPUT, dt, num_rows, ld_dy, 0, mats, offsets != nullptr, n, k, dt, ld_dx, p);
-  if (s != MOE_OK || num_rows == 0 || k == 0) return s;
-  if (!dx || (n > 0 && (!dy || !w))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
-  return run_rows(p, dt, dy, ld_dy, w, k, nullptr, offsets, dx, dt, ld_dx, workspace, workspace_bytes, stream);
+  const moe_status s = plan_backward(dt, num_rows, ld_dy, ld_x, mats, grouped != 0, n, k, want_dx != 0, ld_dx, want_dw != 0, dw_dt, p);
+  if (s == MOE_OK) *out_bytes = p.total;
+  return s;
 }
 
-moe_status moe_linear_rows_dw(const void* dy, moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, const void* x, int64_t ld_x,
-                              const uint8_t* x_codes, const uint8_t* x_scales, int32_t mats, const int32_t* offsets, int64_t n,
-                              int64_t k, void* dw, moe_src_dtype dw_dt, void* workspace, size_t workspace_bytes, void* stream) {
+moe_status moe_linear_rows_backward(const void* dy, moe_src_dtype dt, int64_t num_rows, int64_t ld_dy, const void* x, int64_t ld_x,
+                                    const uint8_t* x_codes, const uint8_t* x_scales, const void* w, int32_t mats,
+                                    const int32_t* offsets, int64_t n, int64_t k, void* dx, int64_t ld_dx, void* dw,
+                                    moe_src_dtype dw_dt, void* workspace, size_t workspace_bytes, void* stream) {
   if (x && (x_codes || x_scales)) return fail(MOE_ERR_INVALID_ARG, "x comes in its own type or in 8 bits, not both");
   if (!x_codes != !x_scales) return fail(MOE_ERR_INVALID_ARG, "codes without scales, or scales without codes");
-  if ((x_codes && ld_x != 0) || (x && ld_x == 0 && k > 0)) return fail(MOE_ERR_INVALID_ARG, "ld_x is 0 for x in 8 bits, and only then");
+  if ((x_codes && ld_x != 0) || (x && dw && ld_x == 0 && k > 0)) return fail(MOE_ERR_INVALID_ARG, "ld_x is 0 for x in 8 bits, and only then");
   RowsCall p;
-  moe_status s = plan_rows(MOE_ROWS_WEIGHT, dt, num_rows, ld_dy, ld_x, mats, offsets != nullptr, n, k, dw_dt, k, p);
-  if (s != MOE_OK || n == 0 || k == 0) return s;
-  if (!dw || (num_rows > 0 && (!dy || !(x || x_codes)))) return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
-  return run_rows(p, dt, dy, ld_dy, x_codes ? x_codes : x, ld_x, x_scales, offsets, dw, dw_dt, k, workspace, workspace_bytes, stream);
+  moe_status s = plan_backward(dt, num_rows, ld_dy, ld_x, mats, offsets != nullptr, n, k, dx != nullptr, ld_dx, dw != nullptr, dw_dt, p);
+  if (s != MOE_OK) return s;
+  if (num_rows == 0 || k == 0) dx = nullptr;  // (nothing to write)
+  if (n == 0 || k == 0) dw = nullptr;
+  if (!dx && !dw) return MOE_OK;
+  if ((num_rows > 0 && n > 0 && !dy) || (dx && n > 0 && !w) || (dw && num_rows > 0 && !x && !x_codes))
+    return fail(MOE_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 2) || !aligned(dw, dw_dt == MOE_SRC_FP32 ? 16 : 2) ||
+      !aligned(offsets, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned buffer (dy, x, w and an fp32 dw: 16 bytes; offsets: 4; else a result's element)");
+  s = check_workspace(p, workspace, workspace_bytes);
+  int num_cus = 0;
+  if (s == MOE_OK) s = check_device(&num_cus);
+  if (s != MOE_OK) return s;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  rows::PadMatrix pads[rows::kMaxPads];
+  int count = 0;
+  if (p.pad_dy) pads[count++] = {dy, num_rows, n, ld_dy, ws + p.off_dy, p.ld_dy};
+  if (p.pad_w && dx) pads[count++] = {w, mats * n, k, k, ws + p.off_w, p.ld_w};
+  if (p.pad_x && !p.codes && dw) pads[count++] = {x, num_rows, k, ld_x, ws + p.off_x, p.ld_x};
+  hipError_t e = count ? rows::launch_pad_rows(pads, count, st) : hipSuccess;
+  if (e == hipSuccess && p.codes && dw)
+    e = launch_dequantize_mx8(x_codes, x_scales, num_rows, k, ws + p.off_x, p.t, p.ld_x, p.ld_x, st);
+  const void* g = p.pad_dy ? ws + p.off_dy : dy;
+  if (e == hipSuccess && dx)
+    e = run_pass(p, Pass::kInput, g, p.ld_dy, p.pad_w ? ws + p.off_w : w, p.ld_w, offsets, dx, p.t, ld_dx, ws, num_cus, st);
+  if (e == hipSuccess && dw)
+    e = run_pass(p, Pass::kWeight, g, p.ld_dy, p.pad_x ? ws + p.off_x : x, p.ld_x, offsets, dw,
+                 dw_dt == MOE_SRC_FP32 ? RowType::kFp32 : p.t, k, ws, num_cus, st);
+  return launched(e);
 }
 
 }  // extern "C"

@@ -244,15 +244,24 @@ struct RowsArgs {
   int slices;
   int num_cus;
 };
+// for few products, operands and their rows anywhere
+hipError_t launch_stream(const RowsArgs& a, const RowsChoice& c, RowType in, hipStream_t st);
 // both operands on 16 bytes with rows on 16 bytes, what they hold between a
 // row's end and its next 16 bytes zero
 hipError_t launch_forward(const RowsArgs& a, const RowsChoice& c, RowType in, RowType out, hipStream_t st);
 hipError_t launch_input(const RowsArgs& a, const RowsChoice& c, RowType in, RowType out, hipStream_t st);
 hipError_t launch_weight(const RowsArgs& a, const RowsChoice& c, RowType in, RowType out, hipStream_t st);
 
-// dst [rows][ld_dst] = src [rows][ld_src] (16-bit elements), zeros from cols to ld_dst
-hipError_t launch_pad_rows(const void* src, int64_t rows, int64_t cols, int64_t ld_src, void* dst, int64_t ld_dst,
-                           hipStream_t st);
+// dst [rows][ld_dst] = src [rows][ld_src] (16-bit elements), zeros from cols to
+// ld_dst, for at most three matrices
+struct PadMatrix {
+  const void* src;
+  int64_t rows, cols, ld_src;
+  void* dst;
+  int64_t ld_dst;
+};
+constexpr int kMaxPads = 3;
+hipError_t launch_pad_rows(const PadMatrix* m, int count, hipStream_t st);
 // out[r] = sum of the slices' row r, rounded once; with offsets, rows of no matrix are zero
 hipError_t launch_join(const float* part, int slices, int64_t rows, int64_t cols, int64_t ld, const int* offsets, int mats,
                        void* out, RowType out_t, int64_t ld_out, hipStream_t st);

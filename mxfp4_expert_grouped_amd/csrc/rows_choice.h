@@ -30,6 +30,7 @@ struct RowsShape {
   int mats;
   bool grouped;         // rows go to the matrices by offsets, else all to the one
   int out_size;         // bytes of an element of C
+  int64_t laid_out;     // elements of operands that are laid out before the tile kernel
   bool pieces;          // a row of C is a whole number of 16-byte pieces, on 16 bytes
 
   int64_t cols() const { return pass == Pass::kForward ? n : k; }
@@ -50,13 +51,19 @@ struct RowsShape {
 };
 
 struct RowsChoice {
-  bool stream;     // k_rows_stream, else k_rows_tile:
+  bool stream;     // k_rows_stream, which reads operands where they are, else k_rows_tile:
   int bm;          // rows of a tile, 64 (not for the weights' gradient), 128 or 256
   int slices;      // parts of L, joined from fp32 sums in the workspace
   bool join;       // through the workspace (slices > 1, or rows that the tile kernel cannot write)
   bool wide;       // rows of C in whole pieces
   int64_t tiles;   // at most so many, slices counted
 };
+
+// Tiles of the smallest kind, with the most that the groups' ends can add.
+inline int64_t least_tiles(const RowsShape& s) {
+  const int64_t tn = ceil_div(s.cols(), kRowsTileN);
+  return (s.pass == Pass::kWeight ? s.mats * ceil_div(s.n, 128) : ceil_div(s.rows, 64) + s.mats) * tn;
+}
 
 // fp32 sums of a slice: rows of C as the tile kernel writes them
 inline int64_t join_rows(const RowsShape& s) { return s.pass == Pass::kWeight ? s.mats * s.n : s.rows; }
@@ -65,6 +72,8 @@ inline int64_t join_ld(const RowsShape& s) { return (s.cols() + 3) & ~int64_t(3)
 inline RowsChoice choose_rows(const RowsShape& s) {
   const int64_t ntn = ceil_div(s.cols(), kRowsTileN), steps = std::max<int64_t>(1, ceil_div(s.length(), 64));
   // By estimates of their times in units of 0.1 us: a step, and a tile's end.
+  // What is not on 16 bytes is laid out first: read and written, at 4 TB/s.
+  const int64_t lay = (s.laid_out * 4 + (s.laid_out ? 800000 : 0)) / 400000;
   static const int kBm[3] = {256, 128, 64}, kStep[3] = {12, 8, 6}, kEnd[3] = {60, 40, 30};
   int64_t best = -1;
   RowsChoice c{};
@@ -72,13 +81,26 @@ inline RowsChoice choose_rows(const RowsShape& s) {
     for (int slices = 1; slices <= kMaxSlices && (slices == 1 || slices * 4 <= steps); slices *= 2) {
       const int64_t tiles = s.row_tiles(kBm[i]) * ntn;
       if (slices > 1 && tiles * slices > 2 * kCus) break;
-      const int64_t join = slices == 1 ? 0 : 50 + join_rows(s) * join_ld(s) * 4 * (slices + 1) / 400000;
+      const int64_t join = slices == 1 ? 0 : 50 + join_rows(s) * join_ld(s) * 8 * slices / 450000;
       const int64_t cost = ceil_div(tiles * slices, kCus) * (ceil_div(steps, slices) * kStep[i] + kEnd[i]) + join;
       if (best < 0 || cost < best) {
         best = cost;
         c.bm = kBm[i];
         c.slices = slices;
       }
+    }
+  }
+  if (s.pass == Pass::kForward) {
+    // 2 us, and 0.18 us per 256 units of 16 x 16 and 128 products
+    const int64_t units = s.row_tiles(16) * ceil_div(s.n, 16);
+    const int64_t stream = 20 + units * ceil_div(s.k, 128) * 18 / 2560;
+    if (stream < best + lay) {
+      c.stream = true;
+      c.slices = 1;
+      c.join = false;
+      c.wide = false;
+      c.tiles = s.row_tiles_max(16) * ceil_div(s.n, 16);
+      return c;
     }
   }
   c.join = c.slices > 1 || (s.out_size == 4 && !s.pieces);

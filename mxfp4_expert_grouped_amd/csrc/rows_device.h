@@ -54,5 +54,10 @@ __device__ __forceinline__ void covered_rows(const int* offsets, int mats, int r
   hi = max(lo, hi);
 }
 
+// whether every row of a matrix is on 16 bytes
+__device__ __forceinline__ bool rows_on_16(const void* p, int64_t ld_bytes) {
+  return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes)) % 16 == 0;
+}
+
 }  // namespace rows
 }  // namespace mxmoe

@@ -99,6 +99,24 @@ __device__ __forceinline__ int tile_matrix(const int* prefix, int mats, int t) {
   return __builtin_amdgcn_readfirstlane(e - 1);
 }
 
+// Zeros in the rows of C that no matrix has, by all workgroups together; part:
+// two words of LDS per wave.
+template <int THREADS, typename TO>
+__device__ __forceinline__ void zero_uncovered(const RowsArgs& a, int* part) {
+  int lo, hi;
+  covered_rows<THREADS>(a.offsets, a.mats, static_cast<int>(a.rows), lo, hi, part);
+  const int none = lo + static_cast<int>(a.rows) - hi;
+  TO* c = static_cast<TO*>(a.c);
+  constexpr int PER = 16 / sizeof(TO);
+  const bool pieces = rows_on_16(c, a.ld_c * sizeof(TO));
+  for (int i = blockIdx.x; i < none; i += gridDim.x) {
+    TO* row = c + (i < lo ? i : i - lo + hi) * a.ld_c;
+    const int whole = pieces ? a.n / PER * PER : 0;
+    for (int x = threadIdx.x * PER; x < whole; x += THREADS * PER) *reinterpret_cast<u32x4*>(row + x) = u32x4{0, 0, 0, 0};
+    for (int x = whole + threadIdx.x; x < a.n; x += THREADS) row[x] = static_cast<TO>(0.0f);
+  }
+}
+
 // Copy of 16 bytes per lane from the buffer's byte off to LDS byte lds + 16
 // lane; a lane whose offset is past the buffer's end brings zeros.  Written as
 // assembly (with no register output) so that the compiler does not wait for it
@@ -616,14 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   if constexpr (PASS != Pass::kWeight) {
     if (!a.offsets || a.slices > 1) return;
     __syncthreads();  // all waves are done with the LDS
-    int lo, hi;
-    covered_rows<kThreads>(a.offsets, a.mats, static_cast<int>(a.rows), lo, hi, reinterpret_cast<int*>(lds));
-    const int none = lo + static_cast<int>(a.rows) - hi;
-    TO* c = static_cast<TO*>(a.c);
-    for (int i = b; i < none; i += G) {
-      TO* row = c + int64_t(i < lo ? i : i - lo + hi) * a.ld_c;
-      for (int x = threadIdx.x; x < a.n; x += kThreads) row[x] = static_cast<TO>(0.0f);
-    }
+    zero_uncovered<kThreads, TO>(a, reinterpret_cast<int*>(lds));
   }
 }
 

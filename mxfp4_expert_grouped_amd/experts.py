@@ -35,7 +35,8 @@ Kept = Tuple[torch.Tensor, torch.Tensor]
 
 _PRODUCT_DTYPES = (torch.bfloat16, torch.float16)
 
-_workspace_bytes = lru_cache(maxsize=1024)(M.moe_linear_rows_workspace_bytes)
+_forward_bytes = lru_cache(maxsize=1024)(M.moe_linear_rows_workspace_bytes)
+_backward_bytes = lru_cache(maxsize=1024)(M.moe_linear_rows_backward_workspace_bytes)
 
 
 def _rows(x: torch.Tensor) -> Tuple[torch.Tensor, int]:
@@ -68,53 +69,48 @@ def _dense(w: torch.Tensor) -> torch.Tensor:
     return w.clone() if w.data_ptr() % 16 and w.numel() else w
 
 
-def _check_product(x: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor], cols: int, what: str) -> Tuple[int, int, int]:
-    """-> (matrices, n, k) of w, for x [R, cols] with cols = ``what`` of w"""
-    if x.dtype not in _PRODUCT_DTYPES:
-        raise ValueError(f"expected bfloat16 or float16 rows, got {x.dtype}")
-    if w.dtype != x.dtype:
-        raise ValueError(f"rows are {x.dtype}, weights {w.dtype}")
+def _check_weights(w: torch.Tensor, offsets: Optional[torch.Tensor], dtype: torch.dtype) -> Tuple[int, int, int]:
+    """-> (matrices, n, k) of w, for rows of type dtype"""
+    if dtype not in _PRODUCT_DTYPES:
+        raise ValueError(f"expected bfloat16 or float16 rows, got {dtype}")
+    if w.dtype != dtype:
+        raise ValueError(f"rows are {dtype}, weights {w.dtype}")
     if w.dim() != (2 if offsets is None else 3):
         raise ValueError(f"weights must be [N, K] without offsets and [E, N, K] with them, got {list(w.shape)}")
-    mats, (n, k) = (1 if offsets is None else w.shape[0]), w.shape[-2:]
-    if x.dim() != 2 or x.shape[1] != (k if what == "K" else n):
-        raise ValueError(f"expected rows [R, {k if what == 'K' else n}], got {list(x.shape)}")
-    _check_offsets(offsets, mats)
-    return mats, n, k
+    return (1, *w.shape) if offsets is None else tuple(w.shape)
 
 
-def _check_offsets(offsets: Optional[torch.Tensor], mats: int) -> None:
-    if offsets is not None and (offsets.dtype is not torch.int32 or offsets.shape != (mats + 1,)):
+def _check_offsets(offsets: Optional[torch.Tensor], mats: int) -> Optional[torch.Tensor]:
+    if offsets is None:
+        return None
+    if offsets.dtype is not torch.int32 or offsets.shape != (mats + 1,):
         raise ValueError(f"offsets must be int32 [{mats + 1}], got {offsets.dtype} {list(offsets.shape)}")
+    return offsets.contiguous()
 
 
-def _workspace(device: torch.device, *shape: int) -> Tuple[Optional[torch.Tensor], int]:
-    need = _workspace_bytes(*shape)
-    return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
+def _scratch(need: int, like: torch.Tensor) -> Optional[torch.Tensor]:
+    return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
 
 
-def _linear(x: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor], back: bool) -> torch.Tensor:
-    """x W^T, or dy W where ``back``"""
-    mats, n, k = _check_product(x, w, offsets, x.shape[-1], "N" if back else "K")
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _linear(x: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor]) -> torch.Tensor:
+    mats, n, k = _check_weights(w, offsets, x.dtype)
+    if x.dim() != 2 or x.shape[1] != k:
+        raise ValueError(f"expected rows [R, {k}], got {list(x.shape)}")
+    offsets = _check_offsets(offsets, mats)
     dev = device_index(x, w, offsets)
     x, ld = _rows(x)
     w = _dense(w)
-    if offsets is not None:
-        offsets = offsets.contiguous()
-    rows, cols = x.shape[0], (k if back else n)
-    out = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
-    dt = ROW_DTYPES[x.dtype]
-    ws, need = _workspace(x.device, M.MOE_ROWS_INPUT if back else M.MOE_ROWS_FORWARD, dt, rows, ld, 0, mats,
-                          offsets is not None, n, k, dt, cols)
-    on_device(dev, M.moe_linear_rows_dx if back else M.moe_linear_rows, x.data_ptr(), dt, rows, ld, w.data_ptr(), mats,
-              None if offsets is None else offsets.data_ptr(), n, k, out.data_ptr(), cols,
-              None if ws is None else ws.data_ptr(), need)
-    return out
-
-
-def linear_dx(dy: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Gradient of :func:`linear` in the rows: dx [R, K] from dy [R, N]; rows of no expert are zero."""
-    return _linear(dy, w, offsets, True)
+    rows, dt = x.shape[0], ROW_DTYPES[x.dtype]
+    y = torch.empty(rows, n, dtype=x.dtype, device=x.device)
+    need = _forward_bytes(dt, rows, ld, mats, offsets is not None, n, k, n)
+    ws = _scratch(need, x)
+    on_device(dev, M.moe_linear_rows, x.data_ptr(), dt, rows, ld, w.data_ptr(), mats, _ptr(offsets), n, k, y.data_ptr(), n,
+              _ptr(ws), need)
+    return y
 
 
 def _is_kept(x) -> bool:
@@ -128,10 +124,6 @@ def _kept(x: Kept, cols: int, scales: int) -> Kept:
     if x[0].shape[1] != cols or x[1].shape != (x[0].shape[0], scales):
         raise ValueError(f"codes {list(x[0].shape)} and scales {list(x[1].shape)} are not [R, {cols}] and [R, {scales}]")
     return x[0].contiguous(), x[1].contiguous()
-
-
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
 
 
 def quantize_mx8(src: torch.Tensor) -> Kept:
@@ -168,45 +160,70 @@ def dequantize_mx8(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype
     return out
 
 
-def linear_dw(dy: torch.Tensor, x: Union[torch.Tensor, Kept], offsets: Optional[torch.Tensor] = None,
-              dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-    """Gradient of :func:`linear` in the weights: dw [E, N, K] (without offsets [N, K]) from dy [R, N] and
-    x [R, K], or x's codes and scales (:func:`quantize_mx8`); of dy's type or float32 (``dtype``).  An expert
-    without rows has a zero gradient."""
+def linear_backward(dy: torch.Tensor, x: Union[torch.Tensor, Kept, None], w: Optional[torch.Tensor],
+                    offsets: Optional[torch.Tensor] = None, need_x: bool = True, need_w: bool = True,
+                    w_dtype: Optional[torch.dtype] = None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of :func:`linear` from dy [R, N]: (dx [R, K] or None, dw [E, N, K], without offsets [N, K], or None).
+
+    dx takes w and is zero in rows of no expert; dw takes x [R, K], or its codes and scales
+    (:func:`quantize_mx8`), and is zero for an expert without rows.  Each may be None where its gradient is not
+    needed.  dw is of dy's type or float32 (``w_dtype``)."""
     if dy.dtype not in _PRODUCT_DTYPES:
         raise ValueError(f"expected bfloat16 or float16 gradients, got {dy.dtype}")
-    dtype = dtype or dy.dtype
-    if dtype not in (dy.dtype, torch.float32):
-        raise ValueError(f"the gradient of the weights is {dy.dtype} or float32, not {dtype}")
     if dy.dim() != 2:
         raise ValueError(f"expected gradients [R, N], got {list(dy.shape)}")
-    if offsets is not None and (offsets.dim() != 1 or offsets.numel() < 2):
-        raise ValueError(f"offsets must be int32 [E + 1], got {list(offsets.shape)}")
-    mats = 1 if offsets is None else offsets.numel() - 1
-    _check_offsets(offsets, mats)
+    w_dtype = w_dtype or dy.dtype
+    if w_dtype not in (dy.dtype, torch.float32):
+        raise ValueError(f"the gradient of the weights is {dy.dtype} or float32, not {w_dtype}")
+    if (need_x and w is None) or (need_w and x is None):
+        raise ValueError("the rows' gradient takes the weights, the weights' gradient the rows")
+    rows, n = dy.shape
+    mats = k = None
+    if need_x:
+        mats, wn, k = _check_weights(w, offsets, dy.dtype)
+        if wn != n:
+            raise ValueError(f"expected gradients [R, {wn}], got {list(dy.shape)}")
+    elif offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError(f"offsets must be int32 [E + 1], got {list(offsets.shape)}")
+        mats = offsets.numel() - 1
+    else:
+        mats = 1
+    offsets = _check_offsets(offsets, mats)
     codes = scales = None
-    if _is_kept(x):
-        codes, scales = _kept(x, x[0].shape[-1], -(-x[0].shape[-1] // 32))
-        rows, k = codes.shape
+    if not need_w:
         x = None
     else:
-        if x.dtype != dy.dtype or x.dim() != 2:
+        if _is_kept(x):
+            codes, scales = _kept(x, x[0].shape[-1], -(-x[0].shape[-1] // 32))
+            x, shape = None, codes.shape
+        elif x.dtype != dy.dtype or x.dim() != 2:
             raise ValueError(f"expected rows [R, K] of type {dy.dtype}, got {x.dtype} {list(x.shape)}")
-        rows, k = x.shape
-    if dy.shape[0] != rows:
-        raise ValueError(f"{dy.shape[0]} rows of gradients for {rows} rows")
-    dev = device_index(dy, x, codes, scales, offsets)
+        else:
+            shape = x.shape
+        if shape[0] != rows or (need_x and shape[1] != k):
+            raise ValueError(f"expected rows [{rows}, {k if need_x else 'K'}], got {list(shape)}")
+        k = shape[1]
+    if not (need_x or need_w):
+        return None, None
+    w = w if need_x else None
+    device_index(dy, w, x, codes, scales, offsets)
+    return _linear_back(dy, x, codes, scales, w, offsets, mats, n, k, need_x, need_w, w_dtype)
+
+
+def _linear_back(dy, x, codes, scales, w, offsets, mats, n, k, need_x, need_w, w_dtype):
+    rows, device = dy.shape[0], dy.device
     dy, ld_dy = _rows(dy)
     x, ld_x = (None, 0) if x is None else _rows(x)
-    if offsets is not None:
-        offsets = offsets.contiguous()
-    n = dy.shape[1]
-    out = torch.empty((n, k) if offsets is None else (mats, n, k), dtype=dtype, device=dy.device)
-    dt, out_dt = ROW_DTYPES[dy.dtype], ROW_DTYPES[dtype]
-    ws, need = _workspace(dy.device, M.MOE_ROWS_WEIGHT, dt, rows, ld_dy, ld_x, mats, offsets is not None, n, k, out_dt, k)
-    on_device(dev, M.moe_linear_rows_dw, dy.data_ptr(), dt, rows, ld_dy, _ptr(x), ld_x, _ptr(codes), _ptr(scales), mats,
-              _ptr(offsets), n, k, out.data_ptr(), out_dt, _ptr(ws), need)
-    return out
+    w = None if w is None else _dense(w)
+    dt, w_dt = ROW_DTYPES[dy.dtype], ROW_DTYPES[w_dtype]
+    dx = torch.empty(rows, k, dtype=dy.dtype, device=device) if need_x else None
+    dw = torch.empty((n, k) if offsets is None else (mats, n, k), dtype=w_dtype, device=device) if need_w else None
+    need = _backward_bytes(dt, rows, ld_dy, ld_x, mats, offsets is not None, n, k, need_x, k, need_w, w_dt)
+    ws = _scratch(need, dy)
+    on_device(dy.get_device(), M.moe_linear_rows_backward, dy.data_ptr(), dt, rows, ld_dy, _ptr(x), ld_x, _ptr(codes), _ptr(scales),
+              _ptr(w), mats, _ptr(offsets), n, k, _ptr(dx), k, _ptr(dw), w_dt, _ptr(ws), need)
+    return dx, dw
 
 
 def _check_checkpoint(checkpoint: Optional[str]) -> bool:
@@ -219,7 +236,9 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets, eight):
         need_x, need_w = x.requires_grad, w.requires_grad
-        y = _linear(x, w, offsets, False)
+        y = _linear(x, w, offsets)
+        ctx.sizes = (1, *w.shape) if offsets is None else w.shape
+        offsets = None if offsets is None else offsets.contiguous()
         kept = () if not need_w else _quantize(x) if eight else (x,)
         ctx.save_for_backward(w if need_x else None, offsets, *kept)
         return y
@@ -228,8 +247,12 @@ class _Linear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         w, offsets, *kept = ctx.saved_tensors
-        dx = linear_dx(dy, w, offsets) if ctx.needs_input_grad[0] else None
-        dw = linear_dw(dy, kept[0] if len(kept) == 1 else kept, offsets) if ctx.needs_input_grad[1] else None
+        # (what came through the forward pass needs no more checks: in the thread that
+        # runs backward passes Python takes several times as long)
+        need_x, need_w = ctx.needs_input_grad[:2]
+        x, codes, scales = (*kept, None, None) if len(kept) == 1 else (None, *kept) if kept else (None, None, None)
+        dx, dw = _linear_back(dy, x if need_w else None, codes, scales, w if need_x else None, offsets, *ctx.sizes, need_x, need_w,
+                              dy.dtype)
         return dx, dw, None, None
 
 
@@ -243,7 +266,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor] = N
     """
     eight = _check_checkpoint(checkpoint)
     if not (torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)):
-        return _linear(x, w, offsets, False)
+        return _linear(x, w, offsets)
     return _Linear.apply(x, w, offsets, eight)
 
 
@@ -267,7 +290,7 @@ def swiglu_backward(da: torch.Tensor, h: Union[torch.Tensor, Kept],
                     need_a: bool = False) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Gradient of :func:`swiglu`: dh [R, 2 d_ff] from da [R, d_ff] and h, or h's codes and scales as
     ``swiglu_keep`` gives them; with ``need_a`` also the activation of that h, else None."""
-    dt = row_dtype(da.dtype)
+    row_dtype(da.dtype)
     if da.dim() != 2:
         raise ValueError(f"expected gradients [R, d_ff], got {list(da.shape)}")
     rows, f = da.shape
@@ -281,12 +304,17 @@ def swiglu_backward(da: torch.Tensor, h: Union[torch.Tensor, Kept],
         h_rows = h.shape[0]
     if h_rows != rows:
         raise ValueError(f"{rows} rows of gradients for {h_rows} rows")
-    dev = device_index(da, h, codes, scales)
+    device_index(da, h, codes, scales)
+    return _swiglu_back(da, h, codes, scales, need_a)
+
+
+def _swiglu_back(da, h, codes, scales, need_a):
+    rows, f = da.shape
     da, ld_da = _strided(da)
     h, ld_h = (None, 0) if h is None else _strided(h)
     dh = torch.empty(rows, 2 * f, dtype=da.dtype, device=da.device)
     a = torch.empty(rows, f, dtype=da.dtype, device=da.device) if need_a else None
-    on_device(dev, M.moe_swiglu_backward, da.data_ptr(), dt, rows, f, ld_da, _ptr(h), ld_h, _ptr(codes), _ptr(scales),
+    on_device(da.get_device(), M.moe_swiglu_backward, da.data_ptr(), ROW_DTYPES[da.dtype], rows, f, ld_da, _ptr(h), ld_h, _ptr(codes), _ptr(scales),
               dh.data_ptr(), 2 * f, _ptr(a), f)
     return dh, a
 
@@ -310,7 +338,8 @@ class _Swiglu(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, da):
         kept = ctx.saved_tensors
-        return swiglu_backward(da, kept[0] if len(kept) == 1 else kept)[0], None
+        h, codes, scales = (*kept, None, None) if len(kept) == 1 else (None, *kept)
+        return _swiglu_back(da, h, codes, scales, False)[0], None
 
 
 def swiglu(h: torch.Tensor, checkpoint: Optional[str] = None) -> torch.Tensor:
@@ -326,9 +355,9 @@ class _Mlp(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate_up, w_down, offsets, eight):
         need_x, need_gu, need_dn = x.requires_grad, w_gate_up.requires_grad, w_down.requires_grad
-        h = _linear(x, w_gate_up, offsets, False)
+        h = _linear(x, w_gate_up, offsets)
         a, kept_h = _swiglu(h, eight)
-        y = _linear(a, w_down, offsets, False)
+        y = _linear(a, w_down, offsets)
         kept_x = () if not need_gu else _quantize(x) if eight else (x,)
         ctx.eight = eight
         # a is not kept: the backward pass has it again from h
@@ -343,13 +372,14 @@ class _Mlp(torch.autograd.Function):
         h, x = (kept[:2], kept[2:]) if ctx.eight else (kept[0], kept[1] if len(kept) > 1 else None)
         need_x, need_gu, need_dn = ctx.needs_input_grad[:3]
         h_width = (h[0] if ctx.eight else h).shape[1]
+        da = None
+        if need_x or need_gu:
+            da, _ = linear_backward(dy, None, w_down, offsets, True, False)
         # (where only w_down has a gradient, a is all that is taken of this)
-        da = linear_dx(dy, w_down, offsets) if need_x or need_gu else dy.new_zeros(dy.shape[0], h_width // 2)
-        dh, a = swiglu_backward(da, h, need_dn)
-        dw_dn = linear_dw(dy, a, offsets) if need_dn else None
-        del a
-        dw_gu = linear_dw(dh, x, offsets) if need_gu else None
-        dx = linear_dx(dh, w_gate_up, offsets) if need_x else None
+        dh, a = swiglu_backward(dy.new_zeros(dy.shape[0], h_width // 2) if da is None else da, h, need_dn)
+        dw_dn = linear_backward(dy, a, None, offsets, False, True)[1] if need_dn else None
+        del a, da
+        dx, dw_gu = linear_backward(dh, x or None if ctx.eight else x, w_gate_up, offsets, need_x, need_gu)
         return dx, dw_gu, dw_dn, None, None
 
 
@@ -365,5 +395,5 @@ def mlp(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, offsets:
     if w_gate_up.shape[-2:-1] != (2 * w_down.shape[-1],) or w_gate_up.shape[:-2] != w_down.shape[:-2]:
         raise ValueError(f"weights {list(w_gate_up.shape)} and {list(w_down.shape)} are not [E, 2 d_ff, K] and [E, M, d_ff]")
     if not (torch.is_grad_enabled() and (x.requires_grad or w_gate_up.requires_grad or w_down.requires_grad)):
-        return _linear(_swiglu(_linear(x, w_gate_up, offsets, False), False)[0], w_down, offsets, False)
+        return _linear(_swiglu(_linear(x, w_gate_up, offsets), False)[0], w_down, offsets)
     return _Mlp.apply(x, w_gate_up, w_down, offsets, eight)

@@ -17,7 +17,6 @@ LIB_PATH = os.path.join(_PKG, "libmxmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
 MOE_SRC_BF16, MOE_SRC_FP32, MOE_SRC_FP16 = 0, 1, 2
 MOE_ID_INT32, MOE_ID_INT64 = 0, 1
-MOE_ROWS_FORWARD, MOE_ROWS_INPUT, MOE_ROWS_WEIGHT = 0, 1, 2
 
 EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_quantize_act",
             "moe_forward", "moe_forward_noalloc", "moe_profile_begin", "moe_profile_end", "moe_packed_scale_bytes",
@@ -26,7 +25,8 @@ EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_quantize
             "moe_quantize_mx4", "moe_dequantize_mx4", "moe_linear_mx4",
             "moe_sort_tokens_workspace_bytes", "moe_sort_tokens", "moe_dispatch_rows",
             "moe_combine_rows", "moe_combine_rows_backward",
-            "moe_linear_rows_workspace_bytes", "moe_linear_rows", "moe_linear_rows_dx", "moe_linear_rows_dw",
+            "moe_linear_rows_workspace_bytes", "moe_linear_rows",
+            "moe_linear_rows_backward_workspace_bytes", "moe_linear_rows_backward",
             "moe_quantize_mx8", "moe_dequantize_mx8", "moe_swiglu", "moe_swiglu_backward",
             "moe_status_string", "moe_last_error")
 STAGES = ("router", "topk", "permute", "gate_up", "down", "combine")
@@ -146,17 +146,20 @@ def load_library(path: str = LIB_PATH):
                                               c_int64, c_void_p, c_void_p, c_int64, c_int32, c_void_p,
                                               c_void_p, c_int64, c_void_p, c_void_p]
     lib.moe_combine_rows_backward.restype = c_int
-    lib.moe_linear_rows_workspace_bytes.argtypes = [c_int, c_int, c_int64, c_int64, c_int64, c_int32, c_int32,
-                                                    c_int64, c_int64, c_int, c_int64, POINTER(c_size_t)]
+    lib.moe_linear_rows_workspace_bytes.argtypes = [c_int, c_int64, c_int64, c_int32, c_int32, c_int64, c_int64,
+                                                    c_int64, POINTER(c_size_t)]
     lib.moe_linear_rows_workspace_bytes.restype = c_int
-    for fn in (lib.moe_linear_rows, lib.moe_linear_rows_dx):
-        fn.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_int64, c_void_p,
-                       c_int64, c_void_p, c_size_t, c_void_p]
-        fn.restype = c_int
-    lib.moe_linear_rows_dw.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
-                                       c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int, c_void_p, c_size_t,
-                                       c_void_p]
-    lib.moe_linear_rows_dw.restype = c_int
+    lib.moe_linear_rows.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_int64,
+                                    c_void_p, c_int64, c_void_p, c_size_t, c_void_p]
+    lib.moe_linear_rows.restype = c_int
+    lib.moe_linear_rows_backward_workspace_bytes.argtypes = [c_int, c_int64, c_int64, c_int64, c_int32, c_int32, c_int64,
+                                                             c_int64, c_int32, c_int64, c_int32, c_int,
+                                                             POINTER(c_size_t)]
+    lib.moe_linear_rows_backward_workspace_bytes.restype = c_int
+    lib.moe_linear_rows_backward.argtypes = [c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                                             c_void_p, c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int64,
+                                             c_void_p, c_int, c_void_p, c_size_t, c_void_p]
+    lib.moe_linear_rows_backward.restype = c_int
     lib.moe_quantize_mx8.argtypes = lib.moe_quantize_mx4.argtypes
     lib.moe_quantize_mx8.restype = c_int
     lib.moe_dequantize_mx8.argtypes = lib.moe_dequantize_mx4.argtypes
@@ -319,11 +322,11 @@ def moe_combine_rows_backward(dy: int, rows: Optional[int], dtype: int, rows_cap
                                                     stream))
 
 
-def moe_linear_rows_workspace_bytes(rows_pass: int, dtype: int, rows: int, ld_a: int, ld_x: int, mats: int, grouped: int,
-                                    n: int, k: int, out_dtype: int, ld_out: int) -> int:
+def moe_linear_rows_workspace_bytes(dtype: int, rows: int, ld_x: int, mats: int, grouped: int, n: int, k: int,
+                                    ld_y: int) -> int:
     out = c_size_t()
-    _check(load_library().moe_linear_rows_workspace_bytes(rows_pass, dtype, rows, ld_a, ld_x, mats, grouped, n, k,
-                                                          out_dtype, ld_out, ctypes.byref(out)))
+    _check(load_library().moe_linear_rows_workspace_bytes(dtype, rows, ld_x, mats, grouped, n, k, ld_y,
+                                                          ctypes.byref(out)))
     return out.value
 
 
@@ -334,19 +337,23 @@ def moe_linear_rows(x: int, dtype: int, rows: int, ld_x: int, w: int, mats: int,
                                           workspace_bytes, stream))
 
 
-def moe_linear_rows_dx(dy: int, dtype: int, rows: int, ld_dy: int, w: int, mats: int, offsets: Optional[int], n: int,
-                       k: int, dx: int, ld_dx: int, workspace: Optional[int], workspace_bytes: int,
-                       stream: Optional[int] = None) -> None:
-    _check(load_library().moe_linear_rows_dx(dy, dtype, rows, ld_dy, w, mats, offsets, n, k, dx, ld_dx, workspace,
-                                             workspace_bytes, stream))
+def moe_linear_rows_backward_workspace_bytes(dtype: int, rows: int, ld_dy: int, ld_x: int, mats: int, grouped: int,
+                                             n: int, k: int, want_dx: int, ld_dx: int, want_dw: int,
+                                             dw_dtype: int) -> int:
+    out = c_size_t()
+    _check(load_library().moe_linear_rows_backward_workspace_bytes(dtype, rows, ld_dy, ld_x, mats, grouped, n, k,
+                                                                   want_dx, ld_dx, want_dw, dw_dtype,
+                                                                   ctypes.byref(out)))
+    return out.value
 
 
-def moe_linear_rows_dw(dy: int, dtype: int, rows: int, ld_dy: int, x: Optional[int], ld_x: int, x_codes: Optional[int],
-                       x_scales: Optional[int], mats: int, offsets: Optional[int], n: int, k: int, dw: int,
-                       dw_dtype: int, workspace: Optional[int], workspace_bytes: int,
-                       stream: Optional[int] = None) -> None:
-    _check(load_library().moe_linear_rows_dw(dy, dtype, rows, ld_dy, x, ld_x, x_codes, x_scales, mats, offsets, n, k, dw,
-                                             dw_dtype, workspace, workspace_bytes, stream))
+def moe_linear_rows_backward(dy: int, dtype: int, rows: int, ld_dy: int, x: Optional[int], ld_x: int,
+                             x_codes: Optional[int], x_scales: Optional[int], w: Optional[int], mats: int,
+                             offsets: Optional[int], n: int, k: int, dx: Optional[int], ld_dx: int, dw: Optional[int],
+                             dw_dtype: int, workspace: Optional[int], workspace_bytes: int,
+                             stream: Optional[int] = None) -> None:
+    _check(load_library().moe_linear_rows_backward(dy, dtype, rows, ld_dy, x, ld_x, x_codes, x_scales, w, mats, offsets,
+                                                   n, k, dx, ld_dx, dw, dw_dtype, workspace, workspace_bytes, stream))
 
 
 def moe_quantize_mx8(src: int, src_dtype: int, rows: int, cols: int, ld_src: int, codes: int, scales: int,

@@ -66,6 +66,18 @@ def data(rows, mats, n, k, dtype, seed):
     return rnd(rows, k), rnd(max(mats, 1), n, k), rnd(rows, n)
 
 
+def dx_of(X, dy, w, off=None):
+    dx, none = X.linear_backward(dy, None, w, off, need_w=False)
+    assert none is None
+    return dx
+
+
+def dw_of(X, dy, x, off=None, dtype=None):
+    none, dw = X.linear_backward(dy, x, None, off, need_x=False, w_dtype=dtype)
+    assert none is None
+    return dw
+
+
 def check_all(X, x, w, dy, offsets, dw_dtype=None):
     """the product and both gradients by the functions without autograd"""
     rows, (mats, n, k) = x.shape[0], w.shape
@@ -73,7 +85,8 @@ def check_all(X, x, w, dy, offsets, dw_dtype=None):
     cuts = offsets if grouped else [0, rows]
     off = torch.tensor(offsets, dtype=torch.int32, device="cuda") if grouped else None
     we = w if grouped else w[0]
-    y, dx, dw = X.linear(x, we, off), X.linear_dx(dy, we, off), X.linear_dw(dy, x, off, dtype=dw_dtype)
+    y, (dx, dw) = X.linear(x, we, off), X.linear_backward(dy, x, we, off, w_dtype=dw_dtype)
+    assert torch.equal(dx, dx_of(X, dy, we, off)) and torch.equal(dw, dw_of(X, dy, x, off, dw_dtype))
     zero = lambda *s: torch.zeros(s, dtype=torch.float64, device="cuda")  # noqa: E731
     ry, my, rdx, mdx, rdw, mdw = zero(rows, n), zero(rows, n), zero(rows, k), zero(rows, k), zero(mats, n, k), zero(mats, n, k)
     for e in range(mats):
@@ -114,14 +127,14 @@ def test_weights_gradient_from_rows_in_8_bits(X, rows, mats, n, k, dtype):
     values = X.dequantize_mx8(*kept, DT[dtype])
     off = torch.tensor(ragged(rows, mats, "uncovered", 1), dtype=torch.int32, device="cuda") if mats else None
     for out in (None, torch.float32):
-        assert torch.equal(X.linear_dw(dy, kept, off, dtype=out), X.linear_dw(dy, values, off, dtype=out))
+        assert torch.equal(dw_of(X, dy, kept, off, out), dw_of(X, dy, values, off, out))
 
 
 def test_rows_with_a_nan_scale_reach_their_columns_only(X):
     x, _, dy = data(40, 2, 16, 70, "bf16", 9)
     x[3, 33] = float("inf")  # in the first matrix
     off = torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda")
-    dw = X.linear_dw(dy, X.quantize_mx8(x), off)
+    dw = dw_of(X, dy, X.quantize_mx8(x), off)
     assert dw[0, :, 32:64].isnan().all() and not dw[0, :, :32].isnan().any() and not dw[0, :, 64:].isnan().any() and not dw[1].isnan().any()
 
 
@@ -129,10 +142,10 @@ def test_rows_of_no_matrix_are_not_read(X):
     # what lies there, NaN included, reaches nothing
     x, w, dy = data(200, 3, 64, 72, "bf16", 2)
     off = torch.tensor([30, 90, 90, 150], dtype=torch.int32, device="cuda")
-    want = X.linear(x, w, off), X.linear_dx(dy, w, off), X.linear_dw(dy, x, off)
+    want = X.linear(x, w, off), dx_of(X, dy, w, off), dw_of(X, dy, x, off)
     for t in (x, dy):
         t[:30], t[150:] = float("nan"), float("inf")
-    got = X.linear(x, w, off), X.linear_dx(dy, w, off), X.linear_dw(dy, x, off)
+    got = X.linear(x, w, off), dx_of(X, dy, w, off), dw_of(X, dy, x, off)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert not want[0][:30].any() and not want[0][150:].any() and not want[1][:30].any() and not want[2][1].any()
 
@@ -140,12 +153,12 @@ def test_rows_of_no_matrix_are_not_read(X):
 def test_views(X):
     x, w, dy = data(120, 3, 128, 96, "bf16", 5)
     off = torch.tensor([0, 50, 70, 120], dtype=torch.int32, device="cuda")
-    want = X.linear(x, w, off), X.linear_dx(dy, w, off), X.linear_dw(dy, x, off)
+    want = X.linear(x, w, off), dx_of(X, dy, w, off), dw_of(X, dy, x, off)
     big = lambda t, left, right: torch.nn.functional.pad(t, (left, right), value=float("nan"))[:, left:left + t.shape[1]]  # noqa: E731
     for xv, wv, dv, ov in ((big(x, 8, 8), w, big(dy, 0, 8), off), (big(x, 3, 2), w, big(dy, 1, 1), off),
                            (x.t().contiguous().t(), w.transpose(1, 2).contiguous().transpose(1, 2), dy.t().contiguous().t(), off),
                            (x, w, dy, torch.stack((off, off), 1)[:, 0]), (x.repeat_interleave(2, 0)[::2], w, dy.repeat_interleave(2, 0)[1::2], off)):
-        got = X.linear(xv, wv, ov), X.linear_dx(dv, wv, ov), X.linear_dw(dv, xv, ov)
+        got = X.linear(xv, wv, ov), dx_of(X, dv, wv, ov), dw_of(X, dv, xv, ov)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
@@ -154,7 +167,7 @@ def test_a_broadcast_gradient(X):
     xl, wl = x.requires_grad_(), w[0].requires_grad_()
     gx, gw = torch.autograd.grad(X.linear(xl, wl).sum(), (xl, wl))
     one = torch.ones(33, 40, dtype=torch.bfloat16, device="cuda")
-    assert torch.equal(gx, X.linear_dx(one, wl.detach())) and torch.equal(gw, X.linear_dw(one, xl.detach()))
+    assert torch.equal(gx, dx_of(X, one, wl.detach())) and torch.equal(gw, dw_of(X, one, xl.detach()))
 
 
 def test_sizes_of_zero(X):
@@ -164,11 +177,11 @@ def test_sizes_of_zero(X):
     assert X.linear(e(4, 8), e(0, 8)).shape == (4, 0)
     assert torch.equal(X.linear(e(4, 0), e(5, 0)), e(4, 5) * 0)
     assert torch.equal(X.linear(e(4, 8), e(3, 5, 8), off), e(4, 5) * 0)
-    assert torch.equal(X.linear_dx(e(4, 0), e(0, 8)), e(4, 8) * 0)
+    assert torch.equal(dx_of(X, e(4, 0), e(0, 8)), e(4, 8) * 0)
     for x in (e(0, 8), X.quantize_mx8(e(0, 8))):
-        assert torch.equal(X.linear_dw(e(0, 5), x), e(5, 8) * 0)
-        assert torch.equal(X.linear_dw(e(0, 5), x, off), e(3, 5, 8) * 0)
-    assert X.linear_dw(e(3, 0), e(3, 8)).shape == (0, 8) and X.linear_dw(e(3, 5), e(3, 0)).shape == (5, 0)
+        assert torch.equal(dw_of(X, e(0, 5), x), e(5, 8) * 0)
+        assert torch.equal(dw_of(X, e(0, 5), x, off), e(3, 5, 8) * 0)
+    assert dw_of(X, e(3, 0), e(3, 8)).shape == (0, 8) and dw_of(X, e(3, 5), e(3, 0)).shape == (5, 0)
 
 
 def test_offsets_out_of_range_stay_inside(X):
@@ -178,4 +191,4 @@ def test_offsets_out_of_range_stay_inside(X):
     tame = torch.tensor([0, 10, 50, 50], dtype=torch.int32, device="cuda")
     y, t = X.linear(x, w, wild), X.linear(x, w, tame)
     assert torch.equal(y, t)
-    assert torch.equal(X.linear_dw(dy, x, wild)[:2], X.linear_dw(dy, x, tame)[:2])
+    assert torch.equal(dw_of(X, dy, x, wild)[:2], dw_of(X, dy, x, tame)[:2])
