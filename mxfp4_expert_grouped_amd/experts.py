@@ -152,8 +152,8 @@ def _quantize(src: torch.Tensor) -> Kept:
 def dequantize_mx8(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values of :func:`quantize_mx8`'s codes [R, C] (moe_dequantize_mx8)."""
     dt = row_dtype(dtype)
-    dev = device_index(codes, scales)
     codes, scales = _kept((codes, scales), codes.shape[-1], -(-codes.shape[-1] // 32))
+    dev = device_index(codes, scales)
     rows, cols = codes.shape
     out = torch.empty(rows, cols, dtype=dtype, device=codes.device)
     on_device(dev, M.moe_dequantize_mx8, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dt, cols)

@@ -104,7 +104,10 @@ def check_all(X, x, w, dy, offsets, dw_dtype=None):
 # rows, matrices (0: one without offsets), n, k
 SIZES = [(1, 0, 1, 1), (1, 0, 8, 8), (3, 0, 64, 64), (64, 0, 256, 64), (65, 0, 257, 65), (300, 0, 512, 320), (1000, 0, 24, 4096),
          (257, 1, 256, 256), (40, 3, 72, 136), (500, 7, 264, 200), (999, 13, 131, 77), (2000, 40, 520, 72), (128, 300, 32, 40),
-         (5000, 3, 128, 128), (700, 2, 1000, 1032), (77, 5, 2, 3), (4096, 9, 384, 640)]
+         (5000, 3, 128, 128), (700, 2, 1000, 1032), (77, 5, 2, 3), (4096, 9, 384, 640),
+         # with those above, every kernel and several tiles for a workgroup (asked of the rule on the CPU)
+         (583, 40, 5593, 40), (1543, 17, 4598, 39), (22940, 0, 1336, 34), (3161, 40, 76, 3296), (1463, 17, 72, 7248),
+         (32685, 40, 94, 36), (8598, 40, 2408, 32), (21, 17, 32, 7776), (9063, 2, 40, 2584)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
