@@ -230,10 +230,11 @@ struct Side {
 // 16-byte pieces.
 //
 // Measured (bf16, 256-row tiles): 8192 x 4096, sums of 7168, forward 345 us
-// (1.39 PF), 8192^3 0.79 ms for each of the three passes (1.39 PF); registers
-// alone reach 1.82 PF on this card, a library's product 1.62, 1.39 and 1.21 PF
-// for the three layouts of 8192^3.  The matrix cores are busy 73 % of the cycles
-// at 1.8 GHz.  What bounds it are the copies: without them (and with wrong
+// (1.39 PF), 8192^3 0.79 ms for each of the three passes (1.39 PF); a library's
+// product reaches 1.62, 1.39 and 1.21 PF for the three layouts of 8192^3.  The
+// matrix cores are busy 73 % of the cycles at 1.8 GHz.  What bounds it is power
+// first: these MFMAs alone, from registers, make 2.48 PF on zeros and 1.79 PF on
+// normal numbers, at 1.7 GHz.  Then the copies: without them (and with wrong
 // results) 1.68 PF, with half of them 1.53, with all of them from lines in L2
 // 1.44, without the LDS reads 1.38; each costs its wave about 30 cycles in which
 // no MFMA is issued.  32768 rows over 64 matrices of 4096 x 7168, uneven:
