@@ -117,10 +117,13 @@ def _is_kept(x) -> bool:
     return isinstance(x, (tuple, list))
 
 
-def _kept(x: Kept, cols: int, scales: int) -> Kept:
-    """Contiguous codes [R, cols] and scales [R, scales]"""
+def _kept(x: Kept, cols: Optional[int] = None, scales: int = 0) -> Kept:
+    """Contiguous codes [R, cols] and scales [R, scales], without cols those of any matrix"""
     if len(x) != 2 or any(t.dtype is not torch.uint8 or t.dim() != 2 for t in x):
         raise ValueError("rows in 8 bits are a pair of uint8 matrices, codes and scales")
+    if cols is None:
+        cols = x[0].shape[1]
+        scales = -(-cols // 32)
     if x[0].shape[1] != cols or x[1].shape != (x[0].shape[0], scales):
         raise ValueError(f"codes {list(x[0].shape)} and scales {list(x[1].shape)} are not [R, {cols}] and [R, {scales}]")
     return x[0].contiguous(), x[1].contiguous()
@@ -152,7 +155,7 @@ def _quantize(src: torch.Tensor) -> Kept:
 def dequantize_mx8(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values of :func:`quantize_mx8`'s codes [R, C] (moe_dequantize_mx8)."""
     dt = row_dtype(dtype)
-    codes, scales = _kept((codes, scales), codes.shape[-1], -(-codes.shape[-1] // 32))
+    codes, scales = _kept((codes, scales))
     dev = device_index(codes, scales)
     rows, cols = codes.shape
     out = torch.empty(rows, cols, dtype=dtype, device=codes.device)
@@ -195,7 +198,7 @@ def linear_backward(dy: torch.Tensor, x: Union[torch.Tensor, Kept, None], w: Opt
         x = None
     else:
         if _is_kept(x):
-            codes, scales = _kept(x, x[0].shape[-1], -(-x[0].shape[-1] // 32))
+            codes, scales = _kept(x)
             x, shape = None, codes.shape
         elif x.dtype != dy.dtype or x.dim() != 2:
             raise ValueError(f"expected rows [R, K] of type {dy.dtype}, got {x.dtype} {list(x.shape)}")
@@ -392,7 +395,7 @@ def mlp(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, offsets:
     activation's input, not its result; with ``checkpoint="mx8"`` both in 8 bits: K + 2 d_ff codes and
     (K + 2 d_ff)/32 scales a row."""
     eight = _check_checkpoint(checkpoint)
-    if w_gate_up.shape[-2:-1] != (2 * w_down.shape[-1],) or w_gate_up.shape[:-2] != w_down.shape[:-2]:
+    if w_gate_up.dim() < 2 or w_down.dim() < 2 or w_gate_up.shape[-2] != 2 * w_down.shape[-1] or w_gate_up.shape[:-2] != w_down.shape[:-2]:
         raise ValueError(f"weights {list(w_gate_up.shape)} and {list(w_down.shape)} are not [E, 2 d_ff, K] and [E, M, d_ff]")
     if not (torch.is_grad_enabled() and (x.requires_grad or w_gate_up.requires_grad or w_down.requires_grad)):
         return _linear(_swiglu(_linear(x, w_gate_up, offsets), False)[0], w_down, offsets)

@@ -204,3 +204,12 @@ def test_a_forward_mode_tangent_is_refused(X):
                      lambda: X.mlp(dual(4, 8), t(6, 8), t(8, 3))):
             with pytest.raises(NotImplementedError, match="tangent"):
                 call()
+
+
+def test_operands_without_dimensions_are_refused(X):
+    u, dy = torch.zeros((), dtype=torch.uint8), t(2, 8)
+    for call in (lambda: X.dequantize_mx8(u, u), lambda: X.linear_backward(dy, (), None, need_x=False),
+                 lambda: X.linear_backward(dy, (u, u), None, need_x=False), lambda: X.swiglu_backward(dy, (u, u)),
+                 lambda: X.mlp(dy, t(), t()), lambda: X.mlp(dy, t(8), t(4)), lambda: X.linear(dy, t())):
+        with pytest.raises(ValueError):
+            call()
