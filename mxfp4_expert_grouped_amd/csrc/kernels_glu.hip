@@ -16,10 +16,11 @@
 //
 // All are bound by memory: a thread moves 8 columns (of gate and up), and four
 // neighbouring lanes share a block and find its largest magnitude with two
-// quad permutes.  131072 rows of d_ff 2048, bf16, kept in 8 bits: 366 us forward
-// and 362 us backward (5.9 TB/s each), in fp16 and 32768 rows kept as they are 67
-// us and 112 us (6.0 TB/s); 8191 rows of 1365 columns in fp32, whose rows and
-// codes lie on no 16 bytes, 32 us and 40 us (4.9 and 3.9 TB/s).
+// quad permutes.  131072 rows of d_ff 2048, bf16, kept in 8 bits: 365 us forward
+// and 365 us backward (calls in a row, 5.9 TB/s each); from a kernel trace, in
+// fp16 and 32768 rows kept as they are 68 us and 117 us (5.9 and 5.7 TB/s), and
+// 8191 rows of 1365 columns in fp32, whose rows and codes lie on no 16 bytes, 33 us
+// and 37 us (4.8 and 4.2 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -7,7 +7,9 @@
 // order.  Bound by the bytes of the weights.  With at most one unit per CU NW
 // is 8 and a wave has the next group's loads on their way while it multiplies
 // this one; with more units NW is 4 and several workgroups per CU hide each
-// other's loads.  1 row x 4096 columns, sums of 7168, bf16: 10 us (5.8 TB/s).
+// other's loads.  1 row x 4096 columns, sums of 7168, bf16, calls in a row: 11.1
+// us on up to four sets of operands in turn, which the Infinity Cache holds (5.3
+// TB/s), and 13.2 us on eight (4.4 TB/s).
 //
 // The weights are the first operand of the 16x16x32 MFMA: lane (r = lane%16,
 // g = lane/16) holds elements 8g .. 8g+7 of row r, and the result of lane l,

@@ -34,6 +34,10 @@ struct RowsShape {
   bool pieces;          // a row of C is a whole number of 16-byte pieces, on 16 bytes
 
   int64_t cols() const { return pass == Pass::kForward ? n : k; }
+  // for the weights' gradient that of an average matrix, since the host does not
+  // know the offsets.  Small matrices of uneven rows are slow for it: 32768 rows of 32
+  // matrices 256 x 128 take 14 us if they are even and 138 us if one has half of
+  // them, as its two tiles then sum on two compute units.
   int64_t length() const { return pass == Pass::kForward ? k : pass == Pass::kInput ? n : rows / std::max(1, mats); }
   // row tiles of bm rows: known for one matrix and for the weights' gradient,
   // otherwise an estimate (the offsets are on the device): half a tile more per
@@ -70,15 +74,16 @@ inline int64_t join_rows(const RowsShape& s) { return s.pass == Pass::kWeight ? 
 inline int64_t join_ld(const RowsShape& s) { return (s.cols() + 3) & ~int64_t(3); }
 
 // Tiles of 256 rows do the most products for what they read, smaller ones fill
-// the chip and a matrix's end better (4096 columns, sums of 7168: 1024 rows 65
-// us in tiles of 64 and 77 in tiles of 128, 2048 rows 101 us in tiles of 128 and
-// 140 in tiles of 256, 8192 rows 345 us in tiles of 256; 32768 rows of 64
-// matrices 1.84 ms in tiles of 256 and 1.90 in tiles of 128).  Few tiles of long
-// sums are cut into slices (64 rows: 21 us with 8 of them, 40 us without; the
-// gradient of one matrix 128 x 256 from 30000 rows 21 us with 64, 98 us with
-// one).  Few products take k_rows_stream (1 row: 12.8 us, 16 us in tiles with 8
-// slices; 64 rows of 64 matrices, one each, 632 against 606 us in tiles, which
-// is why the estimates are close to each other there).
+// the chip and a matrix's end better (captured calls in a row on the same
+// operands; 4096 columns, sums of 7168: 1024 rows 66 us in tiles of 64 and 79 in
+// tiles of 128, 2048 rows 98 us in tiles of 128 and 125 in tiles of 256, 8192 rows
+// 340 us in tiles of 256 and 381 in tiles of 128; 32768 rows of 64 matrices 1.83
+// ms in tiles of 256 and 1.91 in tiles of 128).  Few tiles of long sums are cut
+// into slices (64 rows: 20 us with 8 of them, 23 us with the 16 that are taken, 40
+// us without; the gradient of one matrix 128 x 256 from 30000 rows 21 us with 64,
+// 98 us with one).  Few products take k_rows_stream (1 row: 13 us, 16 us in tiles
+// with 8 or 16 slices; 64 rows of 64 matrices, one each, 632 against 605 us in
+// tiles, which is why the estimates are close to each other there).
 inline RowsChoice choose_rows(const RowsShape& s) {
   const int64_t ntn = ceil_div(s.cols(), kRowsTileN), steps = std::max<int64_t>(1, ceil_div(s.length(), 64));
   // By estimates of their times in units of 0.1 us: a step, and a tile's end.

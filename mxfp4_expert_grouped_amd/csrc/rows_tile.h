@@ -229,17 +229,22 @@ struct Side {
 // TO: element type of C.  WIDE: N and the rows of C are whole numbers of
 // 16-byte pieces.
 //
-// Measured (bf16, 256-row tiles): 8192 x 4096, sums of 7168, forward 345 us
-// (1.39 PF), 8192^3 0.79 ms for each of the three passes (1.39 PF); a library's
-// product reaches 1.62, 1.39 and 1.21 PF for the three layouts of 8192^3.  The
-// matrix cores are busy 73 % of the cycles at 1.8 GHz.  What bounds it is power
-// first: these MFMAs alone, from registers, make 2.48 PF on zeros and 1.79 PF on
-// normal numbers, at 1.7 GHz.  Then the copies: without them (and with wrong
-// results) 1.68 PF, with half of them 1.53, with all of them from lines in L2
-// 1.44, without the LDS reads 1.38; each costs its wave about 30 cycles in which
-// no MFMA is issued.  32768 rows over 64 matrices of 4096 x 7168, uneven:
-// forward 1.84 ms, dx 1.80 ms, dW 2.1 ms, of which 0.68 ms are the stores of
-// its 3.8 GB.
+// Measured (bf16, 256-row tiles, calls in a row on changing operands): 8192 x
+// 4096, sums of 7168, forward 362 us (1.33 PF; short runs on the same operands
+// 340 us), 8192^3 0.81, 0.80 and 0.78 ms for the three passes (1.37 to 1.41 PF); a
+// library's product reaches 1.62, 1.39 and 1.21 PF for the three layouts of
+// 8192^3, under the same power.  What bounds it first are the copies: the matrix
+// cores idle 21 to 28 % of the cycles of 8192^3, and each of a step's 16 copies
+// costs its wave about 30 cycles in which no MFMA is issued, next to 2048 cycles
+// of MFMAs.  Without the copies (and with wrong results) it makes 1.68 PF, with
+// half of them 1.53, with all of them from lines in L2 1.44, without the LDS
+// reads 1.38.  Behind that stands the card's power, which holds the clock at 1.7
+// GHz: these MFMAs alone, from registers, make 1.79 PF on normal numbers and 2.48
+// on zeros.
+// 32768 rows over 64 matrices of 4096 x 7168, uneven: forward 1.82 ms, dx 1.82
+// ms, dW 2.06 ms, of which 0.68 ms are the stores of its 3.8 GB: with two slots
+// half of a step's copies are issued behind the stores of the tile before, and
+// the barrier that needs these copies waits for the stores too.
 template <typename T, typename TO, Pass PASS, int BM, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) k_rows_tile(RowsArgs a) {
   constexpr bool TA = PASS == Pass::kWeight, TB = PASS != Pass::kForward;
