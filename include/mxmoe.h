@@ -461,7 +461,8 @@ moe_status moe_dequantize_mx8(const uint8_t *codes, const uint8_t *scales, int64
 
 /* The gated activation between an expert's projections, row by row:
  *   a = silu(g) u,  g = h[0 .. d_ff), u = h[d_ff .. 2 d_ff), silu(g) = g / (1 + exp(-g))
- * in fp32, rounded once to dt (bf16, fp16 or fp32).  h [rows][ld_h], a
+ * in fp32, rounded once to dt (bf16, fp16 or fp32); for g < -88.7 exp(-g) is
+ * infinite and silu(g) zero, as is its gradient.  h [rows][ld_h], a
  * [rows][ld_a].  codes [rows][2 d_ff] and scales [rows][2 ceil(d_ff/32)] (both
  * or neither): g and u in 8 bits as moe_quantize_mx8 has them, each half with
  * blocks of its own, g's first.

@@ -34,3 +34,19 @@ def test_gates_whose_sigmoid_is_subnormal_from_codes(X):
     got, again = X.swiglu_backward(da.cuda(), kept, need_a=True)
     near(again, a, abs(a))
     near(got, dh, abs(dh))
+
+
+def test_fp32_gates_whose_sigmoid_is_subnormal(X):
+    g = torch.tensor([-87.25, -87.4, -87.9, -88.3, -88.6, -88.7])
+    for up, down in ((2.0 ** 100, 2.0 ** 20), (-(2.0 ** 60), 2.0 ** 62)):
+        h, da = torch.cat((g, torch.full_like(g, up)))[None], torch.full_like(g, down)[None]
+        a, dh, _, _ = ref_swiglu(f64(h)[:, :6], f64(h)[:, 6:], f64(da))
+        near(X.swiglu(h.cuda()), a, abs(a))
+        near(X.swiglu_backward(da.cuda(), h.cuda())[0], dh, abs(dh))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_gates_below_are_zero(X, dtype):
+    g = torch.tensor([-89.0, -95.0, -200.0, -6e4]).to(dtype)
+    h = torch.cat((g, torch.full_like(g, 3.0)))[None].cuda()
+    assert not X.swiglu(h).any() and not X.swiglu_backward(torch.ones(1, 4, dtype=dtype, device="cuda"), h)[0].any()
